@@ -17,6 +17,10 @@ the current stream.  The functions carry the C names:
   q8_0_quantize / q8_0_dequantize / q8_0_nbytes   GGUF Q8_0 blocks
   gguf_a8_requant_q8_0          Q8_0 weight -> int8 / e4m3 codes, one scale per output channel
   gguf_a8_linear                8-bit product with per-channel weight scales -> bf16
+  lora_plan                     which rows of a batch use which low-rank adapter (host -> device, once per batch)
+  lora_forward / lora_backward  adapters of many requests added to a shared projection, and their gradients
+  layer_norm_forward / layer_norm_backward   layer norm over rows, and its gradients
+  w8a8_quant_act_rowwise_layer_norm   row-wise activation quantization of the layer norm, in one pass
   probe_mfma_i8                 diagnostic: sustained int8 MFMA loop (include/w8a8_probe.h)
   probe_cvt_e4m3                diagnostic: the hardware e4m3 conversion on consecutive f32 bit patterns
   probe_gemm_tile_n             diagnostic: the tile width along N w8a8_linear picks for an M x N output
@@ -39,6 +43,7 @@ FP8_E4M3 = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8.h")
+BLOCK_HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8_block.h")
 PROBE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8_probe.h")
 
 
@@ -52,7 +57,7 @@ def _load_library():
             f"{_LIB_PATH} is not built; run `python -m w8a8_quantized_linear_quant_amd.build` "
             "(there is no CPU fallback)")
     lib = ctypes.CDLL(_LIB_PATH)
-    P, I64, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     sigs = {
         "w8a8_status_str": (ctypes.c_char_p, [I]),
         "w8a8_weight_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
@@ -74,6 +79,16 @@ def _load_library():
         "svdq_prepare": (I, [P, I64, I64, I64, P, I, P, P, P, P, P, P]),
         "w8a8_quant_act_rowwise_hadamard": (I, [I, P, I64, I64, I64, P, I64, P, P]),
         "w8a8_hadamard_rotate": (I, [P, I64, I64, I64, P, I64, P]),
+        "lora_plan": (I, [P, P, I64, I64, P, I64, P]),
+        "lora_forward_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+        "lora_forward": (I, [P, I64, I64, I64, P, P, I64, I64, I64, P, P, P, I64, P, I64, P, I64, P, P, P]),
+        "lora_backward_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I64]),
+        "lora_backward": (I, [P, I64, I64, I64, P, I64, I64, P, P, P, I64, I64, P, P, P, I64, P, I64, P, I64, P, P,
+                              P, P]),
+        "layer_norm_forward": (I, [I, P, I64, I64, I64, I, P, P, F, P, I64, P, P, P]),
+        "layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+        "layer_norm_backward": (I, [I, P, I64, P, I64, P, P, I64, I64, I, P, P, I64, P, P, P, P]),
+        "w8a8_quant_act_rowwise_layer_norm": (I, [I, I, P, I64, I64, I64, I, P, P, F, P, I64, P, P, P, P]),
         "w8a8_probe_sink_count": (I64, []),
         "w8a8_probe_mfma_i8": (I, [P, P, I64, P, P]),
         "w8a8_probe_cvt_e4m3": (I, [ctypes.c_uint32, I64, P, P]),
@@ -449,6 +464,236 @@ def gguf_a8_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
     _check(_lib.gguf_a8_linear(qt, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, _ptr(y),
                                _stream(dev)))
     return y
+
+
+# ------------------------------------------------------------------ adapters
+def _view(t, shape, dtype, device, name, align=True):
+    """A matrix operand that may be a view with a row stride, never copied:
+    (data pointer, row stride in elements).  `align`: rows must start on
+    16-byte boundaries."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(0) if rows > 1 else cols
+    ptr = t.data_ptr()
+    if rows > 0 and (ptr % 16 != 0 or (align and ld % 8 != 0)):
+        raise ValueError(f"{name} must start on a 16-byte boundary" +
+                         (f", its rows too (row stride {ld} must be a multiple of 8)" if align else ""))
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride {ld} < {cols})")
+    return ptr, ld
+
+
+def _vec(t, n, dtype, device, name):
+    """A contiguous vector operand of at least n elements, or None: its pointer."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != device or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be contiguous, on {device}, of at least {n} elements")
+    return t.data_ptr()
+
+
+def _gpu_matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
+    return t.device
+
+
+class LoraPlan:
+    """Which rows of a batch use which adapter of a pool (lora_plan).  Holds
+    for one batch; every projection of every layer may share it."""
+
+    __slots__ = ("rows", "adapters", "tiles", "data", "device")
+
+    def __init__(self, rows, adapters, tiles, data):
+        self.rows, self.adapters, self.tiles, self.data, self.device = rows, adapters, tiles, data, data.device
+
+
+def lora_plan(lengths, adapters, num_adapters, device=None):
+    """lengths: rows of each request, in the order of X's rows; adapters: the
+    adapter of each request (0 .. num_adapters - 1, or -1 for none).  Copies
+    the plan to `device` (default: the current GPU)."""
+    lengths, adapters = [int(n) for n in lengths], [int(l) for l in adapters]
+    if len(lengths) != len(adapters):
+        raise ValueError(f"{len(lengths)} lengths, {len(adapters)} adapters")
+    if any(not -1 <= l < num_adapters for l in adapters):
+        raise ValueError(f"adapters must be -1 or in [0, {num_adapters})")
+    S = len(lengths)
+    cl, ca = (ctypes.c_int64 * S)(*lengths), (ctypes.c_int32 * S)(*adapters)
+    tiles = ctypes.c_int64()
+    _check(_lib.lora_plan(cl, ca, S, num_adapters, None, 0, ctypes.byref(tiles)))
+    host = torch.empty(4 * tiles.value + num_adapters + 1, dtype=torch.int32)
+    _check(_lib.lora_plan(cl, ca, S, num_adapters, _ptr(host), host.numel(), ctypes.byref(tiles)))
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return LoraPlan(sum(lengths), num_adapters, tiles.value, host.to(dev))
+
+
+def lora_forward_workspace_bytes(T, K, R):
+    return int(_lib.lora_forward_workspace_bytes(T, K, R))
+
+
+def lora_backward_workspace_bytes(T, K, N, R, L):
+    return int(_lib.lora_backward_workspace_bytes(T, K, N, R, L))
+
+
+def _lora_args(rows, dev, a, b, plan, scale, ranks):
+    if not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan (lora_plan)")
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"a must be [L, R, K] and b [L, N, R], got {tuple(a.shape)} and {tuple(b.shape)}")
+    L, R, K = a.shape
+    if plan.rows != rows or plan.adapters != L or plan.device != dev:
+        raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters on {plan.device}, "
+                         f"the call has {rows} and {L} on {dev}")
+    pa = _vec(a, 0, torch.bfloat16, dev, "a")
+    pb = _vec(b, 0, torch.bfloat16, dev, "b")
+    return L, R, K, b.shape[1], pa, pb, _vec(scale, L, torch.float32, dev, "scale"), _vec(ranks, L, torch.int32, dev,
+                                                                                         "ranks")
+
+
+def lora_forward(x, a, b, plan, scale=None, ranks=None, base=None, out=None, u=None, save_u=True, workspace=None):
+    """Adapters added to a shared projection: x bf16 [M, K]; a bf16 [L, R, K]; b bf16 [L, N, R]; scale f32 [L];
+    ranks int32 [L]; base bf16 [M, N] (the projection's output; `out` may be `base`).
+    Returns (out bf16 [M, N], u f32 [M, R] for lora_backward, or None without save_u).
+    x, base and out may be views with a row stride."""
+    dev = _gpu_matrix(x, "x")
+    M = x.shape[0]
+    L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
+    px, ldx = _view(x, (M, K), torch.bfloat16, dev, "x")
+    pbase, ldbase = (None, 0) if base is None else _view(base, (M, N), torch.bfloat16, dev, "base")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    po, ldo = _view(out, (M, N), torch.bfloat16, dev, "out")
+    if u is None and save_u:
+        u = torch.empty((M, R), dtype=torch.float32, device=dev)
+    pu = None if u is None else _vec(u, M * R, torch.float32, dev, "u")
+    ws = _buf(workspace, lora_forward_workspace_bytes(plan.tiles, K, R), torch.uint8, dev, "workspace", alloc=16)
+    _check(_lib.lora_forward(px, M, K, ldx, pa, pb, L, N, R, ps, pr, plan.data.data_ptr(), plan.tiles, pbase, ldbase,
+                             po, ldo, pu, ws.data_ptr(), _stream(dev)))
+    return out, u
+
+
+def lora_backward(dy, x, u, a, b, plan, scale=None, ranks=None, base=None, out=None, da=None, db=None, need_dx=True,
+                  need_weights=True, workspace=None):
+    """Gradients of lora_forward: dy bf16 [M, N]; x, a, b, plan, scale, ranks of the forward call and its u;
+    base bf16 [M, K]: the shared projection's input gradient (`out` may be `base`).
+    Returns (dx bf16 [M, K], da f32 [L, R, K], db f32 [L, N, R]), None for what is not needed."""
+    dev = _gpu_matrix(dy, "dy")
+    M = dy.shape[0]
+    L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
+    pdy, lddy = _view(dy, (M, N), torch.bfloat16, dev, "dy")
+    px, ldx = _view(x, (M, K), torch.bfloat16, dev, "x")
+    pu = _vec(u, M * R, torch.float32, dev, "u")
+    pbase, ldbase = (None, 0) if base is None else _view(base, (M, K), torch.bfloat16, dev, "base")
+    dx, pdx, lddx = None, None, 0
+    if need_dx:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if out is None else out
+        pdx, lddx = _view(dx, (M, K), torch.bfloat16, dev, "out")
+    if need_weights:
+        if u is None:
+            raise ValueError("u, as lora_forward returned it, is needed for the weights' gradients")
+        da = _out(da, (L, R, K), torch.float32, dev, "da")
+        db = _out(db, (L, N, R), torch.float32, dev, "db")
+    else:
+        da = db = None
+    ws = _buf(workspace, lora_backward_workspace_bytes(plan.tiles, K, N, R, L), torch.uint8, dev, "workspace",
+              alloc=16)
+    _check(_lib.lora_backward(pdy, M, N, lddy, px, K, ldx, pu, pa, pb, L, R, ps, pr, plan.data.data_ptr(), plan.tiles,
+                              pbase, ldbase, pdx, lddx, None if da is None else da.data_ptr(),
+                              None if db is None else db.data_ptr(), ws.data_ptr(), _stream(dev)))
+    return dx, da, db
+
+
+# ---------------------------------------------------------------- layer norm
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _dtype_of(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
+
+
+def _norm_args(x, weight, bias):
+    dev = _gpu_matrix(x, "x")
+    M, K = x.shape
+    xt = _dtype_of(x, "x")
+    px, ldx = _view(x, (M, K), x.dtype, dev, "x", align=False)
+    p = weight if weight is not None else bias
+    wt = xt if p is None else _dtype_of(p, "weight")
+    pw = None if weight is None else _vec(weight, K, weight.dtype, dev, "weight")
+    pb = None if bias is None else _vec(bias, K, weight.dtype if weight is not None else bias.dtype, dev, "bias")
+    return dev, M, K, xt, px, ldx, wt, pw, pb
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
+    """x bf16 or f32 [M, K] (may have a row stride, of any alignment); weight, bias [K] of one dtype (bf16 or f32)
+    or None.  Returns (y like x, mean f32 [M], rstd f32 [M])."""
+    dev, M, K, xt, px, ldx, wt, pw, pb = _norm_args(x, weight, bias)
+    y = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else out
+    py, ldy = _view(y, (M, K), x.dtype, dev, "out", align=False)
+    mean = _buf(mean, M, torch.float32, dev, "mean")
+    rstd = _buf(rstd, M, torch.float32, dev, "rstd")
+    _check(_lib.layer_norm_forward(xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, mean.data_ptr(), rstd.data_ptr(),
+                                   _stream(dev)))
+    return y, mean[:M], rstd[:M]
+
+
+def layer_norm_backward_workspace_bytes(M, K):
+    return int(_lib.layer_norm_backward_workspace_bytes(M, K))
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, dweight=None, dbias=None, need_dx=True,
+                        need_params=None, workspace=None):
+    """Gradients of layer_norm_forward from its x, mean, rstd and weight.  Returns (dx like x, dweight f32 [K],
+    dbias f32 [K]), None for what is not needed (need_params: default, if there is a weight)."""
+    dev, M, K, xt, px, ldx, wt, pw, _ = _norm_args(x, weight, None)
+    pdy, lddy = _view(dy, (M, K), x.dtype, dev, "dy", align=False)
+    pm, pr = _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd")
+    dx, pdx, lddx = None, None, 0
+    if need_dx:
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else out
+        pdx, lddx = _view(dx, (M, K), x.dtype, dev, "out", align=False)
+    if weight is not None if need_params is None else need_params:
+        dweight = _out(dweight, (K,), torch.float32, dev, "dweight")
+        dbias = _out(dbias, (K,), torch.float32, dev, "dbias")
+        ws = _buf(workspace, layer_norm_backward_workspace_bytes(M, K), torch.uint8, dev, "workspace", alloc=16)
+        args = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
+    else:
+        dweight = dbias = None
+        args = None, None, None
+    _check(_lib.layer_norm_backward(xt, pdy, lddy, px, ldx, pm, pr, M, K, wt, pw, pdx, lddx, *args, _stream(dev)))
+    return dx, dweight, dbias
+
+
+def w8a8_quant_act_rowwise_layer_norm(x, weight=None, bias=None, eps=1e-5, qtype=INT8, ldq=None, out=None, scale=None,
+                                      mean=None, rstd=None):
+    """Row-wise quantization of layer_norm_forward's f32 values: (codes [M, ldq], scales f32 [M]).  `mean` and
+    `rstd` f32 [M] are written if passed in."""
+    cd = _code_dtype(qtype)
+    dev, M, K, xt, px, ldx, wt, pw, pb = _norm_args(x, weight, bias)
+    ldq = ldq if ldq is not None else K + (-K) % 16
+    xq = _out(out, (M, ldq), cd, dev, "out")
+    s = _buf(scale, M, torch.float32, dev, "scale")
+    _check(_lib.w8a8_quant_act_rowwise_layer_norm(
+        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, s.data_ptr(),
+        _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd"), _stream(dev)))
+    return xq, s[:M]
 
 
 # ---------------------------------------------------------------- diagnostics
