@@ -68,13 +68,13 @@ w8a8_status lora_plan(const int64_t *lengths, const int32_t *adapters, int64_t S
  *   whatever they hold.  plan: device copy of lora_plan's T tiles.
  *   base bf16 [M, ldbase] or NULL (0); out bf16 [M, ldout], may be base
  *   (in place, same stride).  u f32 [M, R] or NULL: what lora_backward takes.
- *   workspace lora_forward_workspace_bytes(T, K, R) bytes.
+ *   workspace lora_forward_workspace_bytes(M, R) bytes, used if u is NULL.
  * Rows in no tile are not written.
  * Shape rules: M >= 0, T >= 0, 1 <= L <= 65535; K, N, R, strides multiples of
  * 8; 8 <= R <= 128 (else W8A8_ERR_INVALID_ARG), 8 <= K, N <= 2^22,
  * M <= 2^30, strides from their width up to 2^22.
  */
-size_t lora_forward_workspace_bytes(int64_t T, int64_t K, int64_t R);
+size_t lora_forward_workspace_bytes(int64_t M, int64_t R);
 w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint16_t *a, const uint16_t *b,
                          int64_t L, int64_t N, int64_t R, const float *scale, const int32_t *ranks,
                          const int32_t *plan, int64_t T, const uint16_t *base, int64_t ldbase, uint16_t *out,
@@ -92,10 +92,10 @@ w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, c
  *   projection's own input gradient (w8a8_linear_backward_dx), may be dx.
  *   dx bf16 [M, lddx]; da f32 [L, R, K]; db f32 [L, N, R], f32 accurate.
  *   dx may be NULL (no input gradient); da and db may both be NULL.
- *   workspace lora_backward_workspace_bytes(T, K, N, R, L) bytes.
+ *   workspace lora_backward_workspace_bytes(M, T, K, N, R, L) bytes.
  * Shape rules as lora_forward.
  */
-size_t lora_backward_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L);
+size_t lora_backward_workspace_bytes(int64_t M, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L);
 w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, int64_t lddy, const uint16_t *x, int64_t K,
                           int64_t ldx, const float *u, const uint16_t *a, const uint16_t *b, int64_t L, int64_t R,
                           const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T,

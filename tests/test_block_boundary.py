@@ -102,7 +102,7 @@ def test_lora_refuses_sizes(f):
 
 def test_lora_refuses_pointers():
     assert _forward(x=NULL) == INVALID and _forward(out=NULL) == INVALID and _forward(plan=NULL) == INVALID
-    assert _forward(ws=NULL) == INVALID and _forward(a=NULL) == INVALID
+    assert _forward(u=NULL, ws=NULL) == INVALID and _forward(a=NULL) == INVALID and _forward(ws=MIS) == ALIGN
     assert _forward(x=MIS) == ALIGN and _forward(out=MIS) == ALIGN and _forward(u=MIS) == ALIGN
     assert _forward(base=MIS) == ALIGN and _forward(ranks=MIS) == ALIGN and _forward(plan=MIS) == ALIGN
     assert _forward(ldo=60) == SHAPE
@@ -115,11 +115,11 @@ def test_lora_refuses_pointers():
 
 
 def test_lora_workspace_sizes():
-    assert w8.lora_forward_workspace_bytes(0, 64, 16) >= 0
-    assert lib.lora_forward_workspace_bytes(-1, 64, 16) == 0 and lib.lora_forward_workspace_bytes(1, 64, 129) == 0
-    one, two = (w8.lora_backward_workspace_bytes(t, 64, 64, 16, 1) for t in (1, 2))
-    assert 0 < one <= two
-    assert lib.lora_backward_workspace_bytes(1, 64, 64, 16, 0) == 0
+    assert w8.lora_forward_workspace_bytes(0, 16) == 0 and w8.lora_forward_workspace_bytes(5, 16) == 5 * 16 * 4
+    assert lib.lora_forward_workspace_bytes(-1, 16) == 0 and lib.lora_forward_workspace_bytes(1, 129) == 0
+    one, many = (w8.lora_backward_workspace_bytes(64 * t, t, 64, 64, 16, 1) for t in (1, 100))
+    assert 64 * 16 * 4 <= one < many
+    assert lib.lora_backward_workspace_bytes(64, 1, 64, 64, 16, 0) == 0
 
 
 def _norm(xt=0, x=A, M=4, K=64, ldx=64, wt=0, w=A, b=A, eps=1e-5, y=A, ldy=64, mean=A, rstd=A):

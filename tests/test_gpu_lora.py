@@ -275,8 +275,8 @@ def test_same_bits_every_time_and_under_graph_capture(w8):
     x, dy, base, dbase = t.x.cuda(), t.dy.cuda(), t.base.cuda(), t.dbase.cuda()
     out, u = torch.empty_like(base), torch.empty(t.M, 32, device="cuda")
     dx, da, db = torch.empty_like(dbase), torch.empty(3, 32, 512, device="cuda"), torch.empty(3, 768, 32, device="cuda")
-    fw = torch.empty(w8.lora_forward_workspace_bytes(d["plan"].tiles, 512, 32) + 16, dtype=torch.uint8, device="cuda")
-    bw = torch.empty(w8.lora_backward_workspace_bytes(d["plan"].tiles, 512, 768, 32, 3) + 16, dtype=torch.uint8,
+    fw = torch.empty(w8.lora_forward_workspace_bytes(t.M, 32), dtype=torch.uint8, device="cuda")
+    bw = torch.empty(w8.lora_backward_workspace_bytes(t.M, d["plan"].tiles, 512, 768, 32, 3), dtype=torch.uint8,
                      device="cuda")
 
     def step():

@@ -80,9 +80,9 @@ def _load_library():
         "w8a8_quant_act_rowwise_hadamard": (I, [I, P, I64, I64, I64, P, I64, P, P]),
         "w8a8_hadamard_rotate": (I, [P, I64, I64, I64, P, I64, P]),
         "lora_plan": (I, [P, P, I64, I64, P, I64, P]),
-        "lora_forward_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+        "lora_forward_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
         "lora_forward": (I, [P, I64, I64, I64, P, P, I64, I64, I64, P, P, P, I64, P, I64, P, I64, P, P, P]),
-        "lora_backward_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I64]),
+        "lora_backward_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I64, I64]),
         "lora_backward": (I, [P, I64, I64, I64, P, I64, I64, P, P, P, I64, I64, P, P, P, I64, P, I64, P, I64, P, P,
                               P, P]),
         "layer_norm_forward": (I, [I, P, I64, I64, I64, I, P, P, F, P, I64, P, P, P]),
@@ -542,12 +542,12 @@ def lora_plan(lengths, adapters, num_adapters, device=None):
     return LoraPlan(sum(lengths), num_adapters, tiles.value, host.to(dev))
 
 
-def lora_forward_workspace_bytes(T, K, R):
-    return int(_lib.lora_forward_workspace_bytes(T, K, R))
+def lora_forward_workspace_bytes(M, R):
+    return int(_lib.lora_forward_workspace_bytes(M, R))
 
 
-def lora_backward_workspace_bytes(T, K, N, R, L):
-    return int(_lib.lora_backward_workspace_bytes(T, K, N, R, L))
+def lora_backward_workspace_bytes(M, T, K, N, R, L):
+    return int(_lib.lora_backward_workspace_bytes(M, T, K, N, R, L))
 
 
 def _lora_args(rows, dev, a, b, plan, scale, ranks):
@@ -581,9 +581,12 @@ def lora_forward(x, a, b, plan, scale=None, ranks=None, base=None, out=None, u=N
     if u is None and save_u:
         u = torch.empty((M, R), dtype=torch.float32, device=dev)
     pu = None if u is None else _vec(u, M * R, torch.float32, dev, "u")
-    ws = _buf(workspace, lora_forward_workspace_bytes(plan.tiles, K, R), torch.uint8, dev, "workspace", alloc=16)
+    pws = None
+    if u is None or workspace is not None:
+        workspace = _buf(workspace, lora_forward_workspace_bytes(M, R), torch.uint8, dev, "workspace", alloc=16)
+        pws = workspace.data_ptr()
     _check(_lib.lora_forward(px, M, K, ldx, pa, pb, L, N, R, ps, pr, plan.data.data_ptr(), plan.tiles, pbase, ldbase,
-                             po, ldo, pu, ws.data_ptr(), _stream(dev)))
+                             po, ldo, pu, pws, _stream(dev)))
     return out, u
 
 
@@ -610,8 +613,8 @@ def lora_backward(dy, x, u, a, b, plan, scale=None, ranks=None, base=None, out=N
         db = _out(db, (L, N, R), torch.float32, dev, "db")
     else:
         da = db = None
-    ws = _buf(workspace, lora_backward_workspace_bytes(plan.tiles, K, N, R, L), torch.uint8, dev, "workspace",
-              alloc=16)
+    ws = _buf(workspace, lora_backward_workspace_bytes(M, plan.tiles, K, N, R, L), torch.uint8, dev,
+              "workspace", alloc=16)
     _check(_lib.lora_backward(pdy, M, N, lddy, px, K, ldx, pu, pa, pb, L, R, ps, pr, plan.data.data_ptr(), plan.tiles,
                               pbase, ldbase, pdx, lddx, None if da is None else da.data_ptr(),
                               None if db is None else db.data_ptr(), ws.data_ptr(), _stream(dev)))

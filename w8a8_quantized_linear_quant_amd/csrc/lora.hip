@@ -4,16 +4,20 @@
 //   u = s_l x A_l^T           (down, over K)       out = base + u B_l^T   (up)
 //   g = s_l dy B_l            (down, over N)       dx  = base + g A_l     (up)
 //   dA_l = sum_m g^T x        dB_l = sum_m dy^T u  (over the rows of l)
-// Three forms in all: a down-projection of the rows, an up-projection added to
-// a base, and a sum of outer products over an adapter's rows.  The weight of a
-// form is A [R, K] or B [N, R]; the strides (sj, sc) of the rank index j and
-// the wide index c tell them apart.
+// Three kernels in all, each on the bf16 MFMA: a down-projection of the rows,
+// an up-projection added to a base, and a sum of outer products over an
+// adapter's rows.  The weight of the first two is A [R, K] or B [N, R]: one of
+// the two has the MFMA's contraction index contiguous in memory, the other
+// (TR) is transposed on its way to the registers.
+//
+// All three are bound by streaming the wide tensors (x, dy, base, out): R is
+// small, so each takes 2 R operations for the 2 bytes of an element, far below
+// the 500 or so at which the matrix pipes would be the bound.
 #include "block.hpp"
 
 namespace w8a8 {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTileRows = W8A8_LORA_TILE_ROWS;
 constexpr int kMaxR = 128;
 constexpr int64_t kMaxL = 65535;
@@ -33,73 +37,450 @@ __device__ __forceinline__ Tile load_tile(const int32_t *plan, int t, int64_t M,
 }
 
 __device__ __forceinline__ int rank_of(const int32_t *ranks, int l, int R) {
-    return ranks ? min(max(ranks[l], 0), R) : R;
+    return l < 0 ? 0 : ranks ? min(max(ranks[l], 0), R) : R;
 }
 
-// One workgroup per tile: p[t][row][j], and u[m][j] if wanted.
-__global__ __launch_bounds__(kThreads) void lora_down_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
-                                                             const uint16_t *w, int64_t wl, int64_t sj, int64_t sc,
-                                                             int L, int R, const float *scale, const int32_t *ranks,
-                                                             const int32_t *plan, float *p, float *u) {
-    const Tile tile = load_tile(plan, blockIdx.x, M, L);
+// A buffer of `rows` rows of `cols` bf16 elements, ld apart, from row0: reads
+// past the last row's end give 0.  The base is 64-bit, the offsets inside a
+// tile are below 2^31 (64 rows of at most 2^22 elements).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t *p, int64_t row0, int rows, int64_t ld,
+                                                            int cols) {
+    const int bytes = rows > 0 ? (int)(((rows - 1) * ld + cols) * 2) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p) + row0 * ld, (short)0, bytes, kBufferRsrcWord3);
+}
+// The rows of a tile in v f32 [M, R].
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rsrc(const float *v, int64_t row0, int rows, int R) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(v) + row0 * R, (short)0, rows * R * 4, kBufferRsrcWord3);
+}
+__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, int offset) {
+    return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+}
+__device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// Lanes: MFMA 16x16x32, A row (and B column) lane % 16, contraction elements
+// 8 (lane / 16) .. + 7; D row 4 (lane / 16) + e, column lane % 16.
+
+// ---------------------------------------------------------------- down
+// One workgroup takes 16 RB rows of a tile over all of C: 16 waves split the
+// 32-wide steps of the contraction (pairs of steps, so that a wave reads whole
+// 128-byte lines), U steps' loads in flight at a time, and their sums meet in
+// LDS.  No partial sums leave the workgroup.  JB: 16-wide blocks of the rank.
+constexpr int kDownWaves = 16;
+
+// TR's weight fragments: 32 rows n of B by 16 JB ranks go through a wave's own
+// piece of LDS and come back transposed (ds_read_b64_tr_b16: each 16 lanes
+// read 4 rows of 16 columns, lane i receives column i's 4 values).
+template <int JB>
+__device__ __forceinline__ void stage_transposed(uint16_t *area, const v4u (&d)[JB], int lane) {
+#pragma unroll
+    for (int i = 0; i < JB; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 8) = d[i];
+}
+template <int JB>
+__device__ __forceinline__ v4u transposed_fragment(uint16_t *area, int jb, int lane) {
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const int g = lane >> 4, q = lane & 15;
+    uint16_t *p = area + (8 * g + q / 4) * (16 * JB) + jb * 16 + (q % 4) * 4;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * 16 * JB));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return v4u{a.x, a.y, b.x, b.y};
+}
+
+template <int JB, int RB, bool TR>
+__global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
+                                                                    const uint16_t *w, int L, int R,
+                                                                    const float *scale, const int32_t *ranks,
+                                                                    const int32_t *plan, float *v) {
+    constexpr int U = JB * RB <= 2 ? 4 : JB <= 4 ? 2 : 1;
+    constexpr int kStage = TR ? kDownWaves * U * JB * 512 * 2 : 0;            // bytes
+    constexpr int kSums = kDownWaves * RB * 16 * 17 * 4;
+    __shared__ __attribute__((aligned(16))) char lds[kStage > kSums ? kStage : kSums];
+    constexpr int kParts = 4 / RB;
+    const Tile tile = load_tile(plan, blockIdx.x / kParts, M, L);
+    const int first = (blockIdx.x % kParts) * (16 * RB);
+    if (first >= tile.rows) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = tile.adapter < 0 ? 0 : rank_of(ranks, tile.adapter, R);
-    for (int i = wave; i < kTileRows * R; i += kThreads / 64) {
-        const int row = i / R, j = i % R;
-        float s = 0.f;
-        if (row < tile.rows && j < r) {
-            const uint16_t *xr = x + (tile.row0 + row) * ldx;
-            const uint16_t *wr = w + tile.adapter * wl + j * sj;
-            for (int c = lane; c < C; c += 64) s = __builtin_fmaf(bf16_bits_to_f32(xr[c]), bf16_bits_to_f32(wr[c * sc]), s);
-            s = wave_sum(s) * (scale ? scale[tile.adapter] : 1.f);
+    const int r = rank_of(ranks, tile.adapter, R);
+    v4f acc[RB][JB];
+#pragma unroll
+    for (int a = 0; a < RB; ++a)
+#pragma unroll
+        for (int b = 0; b < JB; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    if (r > 0) {  // the same for the whole workgroup
+        const auto rx = rows_rsrc(x, tile.row0 + first, tile.rows - first, ldx, C);
+        const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)tile.adapter * R * C, (short)0,
+                                                          R * C * 2, kBufferRsrcWord3);
+        const int fi = lane & 15, fg = lane >> 4;
+        uint16_t *area = reinterpret_cast<uint16_t *>(lds) + wave * (U * JB * 512);
+        const int steps = (C + 31) / 32;
+        // this wave's n-th step: 2 wave + (n & 1) + 32 (n / 2)
+        for (int n = 0; 2 * wave + 16 * (n & ~1) < steps; n += U) {
+            v4u xf[U][RB], wf[U][JB];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int s = U == 1 ? 2 * wave + (n & 1) + (n & ~1) * 16 : 2 * wave + (i & 1) + (n + (i & ~1)) * 16;
+                const int k = s * 32 + fg * 8;
+                // past C both factors read 0: neither may be whatever lies behind a row
+#pragma unroll
+                for (int a = 0; a < RB; ++a)
+                    xf[i][a] = load16(rx, k < C ? (int)((a * 16 + fi) * ldx + k) * 2 : kOobOffset);
+#pragma unroll
+                for (int b = 0; b < JB; ++b) {
+                    if constexpr (TR) {
+                        const int c = b * 64 + lane, row = s * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
+                        wf[i][b] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
+                    } else {
+                        wf[i][b] = load16(rw, k < C ? ((b * 16 + fi) * C + k) * 2 : kOobOffset);
+                    }
+                }
+            }
+            if constexpr (TR) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) stage_transposed<JB>(area + i * JB * 512, wf[i], lane);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int b = 0; b < JB; ++b) {
+                    const v4u f = TR ? transposed_fragment<JB>(area + i * JB * 512, b, lane) : wf[i][b];
+#pragma unroll
+                    for (int a = 0; a < RB; ++a) acc[a][b] = mfma(xf[i][a], f, acc[a][b]);
+                }
         }
-        if (lane == 0) {
-            p[((int64_t)blockIdx.x * kTileRows + row) * R + j] = s;
-            if (u && row < tile.rows) u[(tile.row0 + row) * R + j] = s;
+    }
+    const float s = tile.adapter >= 0 && scale ? scale[tile.adapter] : 1.f;
+    auto part = reinterpret_cast<float (*)[RB * 16][17]>(lds);
+#pragma unroll
+    for (int b = 0; b < JB; ++b) {
+        __syncthreads();
+#pragma unroll
+        for (int a = 0; a < RB; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[wave][a * 16 + 4 * (lane >> 4) + e][lane & 15] = acc[a][b][e];
+        __syncthreads();
+        const int row = threadIdx.x / 16, j = b * 16 + threadIdx.x % 16;
+        if (row < RB * 16 && first + row < tile.rows && j < R) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < kDownWaves; ++k) t += part[k][row][threadIdx.x % 16];
+            v[(tile.row0 + first + row) * R + j] = j < r ? t * s : 0.f;
         }
     }
 }
 
-// One workgroup per tile and 256 columns.
-__global__ __launch_bounds__(kThreads) void lora_up_kernel(const float *p, const uint16_t *w, int64_t wl, int64_t sj,
-                                                           int64_t sc, int64_t M, int C, int L, int R,
-                                                           const int32_t *ranks, const int32_t *plan,
-                                                           const uint16_t *base, int64_t ldbase, uint16_t *out,
-                                                           int64_t ldout) {
-    const Tile tile = load_tile(plan, blockIdx.x, M, L);
-    const int c = blockIdx.y * kThreads + threadIdx.x;
-    if (c >= C) return;
-    const int r = tile.adapter < 0 ? 0 : rank_of(ranks, tile.adapter, R);
-    for (int row = 0; row < tile.rows; ++row) {
-        const float *pr = p + ((int64_t)blockIdx.x * kTileRows + row) * R;
-        float s = base ? bf16_bits_to_f32(base[(tile.row0 + row) * ldbase + c]) : 0.f;
-        for (int j = 0; j < r; ++j) s = __builtin_fmaf(pr[j], bf16_bits_to_f32(w[tile.adapter * wl + j * sj + c * sc]), s);
-        Bf16::store(out + (tile.row0 + row) * ldout + c, s);
+// ------------------------------------------------------------------ up
+// D^T = W v^T: the MFMA's rows are columns of the output, its columns the
+// tile's rows, so that a lane holds 8 consecutive columns of one row and base
+// and out move as 16-byte accesses.  A wave takes 128 columns (8 MFMAs: MFMA t
+// has column 8 pi(i) + t as its row i, pi(4 g + e) = 4 e + g) of all the
+// tile's rows, with its weights in registers.  v is two bf16 halves (hi + lo,
+// ~16 bits); up to R = 16 both fit one 32-wide contraction, the weight twice.
+constexpr int kUpWaves = 4;
+
+// Eight f32 values as bf16 halves; lo = 0 beside an infinite hi.
+__device__ __forceinline__ void split2(const float *f, v4u &hi, v4u &lo) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        hi[p] = pack_bf16x2(f[2 * p], f[2 * p + 1]);
+        const float a = __uint_as_float(hi[p] << 16), b = __uint_as_float(hi[p] & 0xFFFF0000u);
+        lo[p] = pack_bf16x2(__builtin_isfinite(a) ? f[2 * p] - a : 0.f, __builtin_isfinite(b) ? f[2 * p + 1] - b : 0.f);
     }
 }
 
-// One thread per (j, c) of an adapter: the sum over its rows of v[m][j] y[m][c],
-// v = u[m][j] (by row) or the down-projection's p[t][row][j] (by tile).
-__global__ __launch_bounds__(kThreads) void lora_outer_kernel(const float *u, const float *p, const uint16_t *y,
-                                                              int64_t M, int C, int64_t ldy, int L, int R,
-                                                              const int32_t *ranks, const int32_t *plan, int T,
-                                                              int64_t sj, int64_t sc, float *d) {
-    const int l = blockIdx.z, j = blockIdx.y, c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= C) return;
-    const int32_t *first = plan + 4 * (int64_t)T;
-    float s = 0.f;
-    if (j < rank_of(ranks, l, R)) {
-        const int t1 = min(first[l + 1], T);
-        for (int t = max(first[l], 0); t < t1; ++t) {
-            const Tile tile = load_tile(plan, t, M, L);
-            for (int row = 0; row < tile.rows; ++row) {
-                const int64_t m = tile.row0 + row;
-                const float v = u ? u[m * R + j] : p[((int64_t)t * kTileRows + row) * R + j];
-                s = __builtin_fmaf(v, bf16_bits_to_f32(y[m * ldy + c]), s);
+// The 16-bit halves of (a, b): the low ones, or the high ones.
+__device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, bool high) {
+    return __builtin_amdgcn_perm(b, a, high ? 0x07060302u : 0x05040100u);
+}
+
+template <int JB, bool TR>
+__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
+                                                                int L, int R, const int32_t *ranks,
+                                                                const int32_t *plan, int groups, const uint16_t *base,
+                                                                int64_t ldbase, uint16_t *out, int64_t ldout) {
+    constexpr int KB = JB == 1 ? 1 : JB / 2;  // 32-wide contractions
+    constexpr int RB = kTileRows / 16;
+    const Tile tile = load_tile(plan, blockIdx.x / groups, M, L);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col0 = (blockIdx.x % groups * kUpWaves + wave) * 128;
+    if (tile.rows == 0 || col0 >= C) return;
+    const int r = rank_of(ranks, tile.adapter, R);
+    const int fi = lane & 15, fg = lane >> 4;
+    const int jg = JB == 1 ? fg & 1 : fg;  // this lane's 8 ranks of a contraction
+
+    // base, for all the row blocks at once
+    v4u bf[RB][4];
+    const auto rb = rows_rsrc(base, tile.row0, base ? tile.rows : 0, ldbase, C);
+#pragma unroll
+    for (int a = 0; a < RB; ++a) {
+        if (a * 16 >= tile.rows) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bf[a][e] = load16(rb, (int)((a * 16 + fi) * ldbase + col0 + 8 * (4 * e + fg)) * 2);
+    }
+    // weight fragments: entries beyond the adapter's rank are 0, whatever lies there
+    v4u wf[8][KB];
+    if (r > 0) {
+        const uint16_t *wl = w + (int64_t)tile.adapter * R * C;
+        const int ci = col0 + 8 * (4 * (fi & 3) + (fi >> 2));
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int j = k * 32 + jg * 8;
+            if constexpr (TR) {
+                const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, r * C * 2, kBufferRsrcWord3);
+                v4u d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = load16(rw, ci < C ? ((j + i) * C + ci) * 2 : kOobOffset);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) wf[t][k][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
+            } else {
+                const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, R * C * 2, kBufferRsrcWord3);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) wf[t][k] = load16(rw, ci + t < C && j < R ? ((ci + t) * R + j) * 2 : kOobOffset);
+                if (r < R) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const uint32_t keep = (j + 2 * p < r ? 0xFFFFu : 0u) | (j + 2 * p + 1 < r ? 0xFFFF0000u : 0u);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) wf[t][k][p] &= keep;
+                    }
+                }
             }
         }
     }
-    d[(int64_t)l * R * C + j * sj + c * sc] = s;
+    const auto rv = v_rsrc(v, tile.row0, tile.rows, R);
+#pragma unroll
+    for (int a = 0; a < RB; ++a) {
+        if (a * 16 >= tile.rows) break;
+        v4f acc[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[t][e] = __uint_as_float(t & 1 ? bf[a][e][t / 2] & 0xFFFF0000u : bf[a][e][t / 2] << 16);
+        if (r > 0) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const int j = k * 32 + jg * 8, at = j < R ? ((a * 16 + fi) * R + j) * 4 : kOobOffset;
+                const v4u d0 = load16(rv, at), d1 = load16(rv, at + 16);
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(d0[i]), f[4 + i] = __uint_as_float(d1[i]);
+                v4u hi, lo;
+                split2(f, hi, lo);
+                if constexpr (JB == 1) {
+                    const v4u h = fg < 2 ? hi : lo;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], h, acc[t]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], hi, acc[t]);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], lo, acc[t]);
+                }
+            }
+        }
+        if (a * 16 + fi < tile.rows) {
+            uint16_t *o = out + (tile.row0 + a * 16 + fi) * ldout + col0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 8 * (4 * e + fg);
+                if (col0 + c >= C) continue;
+                v4u d;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
+                *reinterpret_cast<v4u *>(o + c) = d;
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- outer sums
+// d[c][j] = sum over an adapter's rows of y[m][c] v[m][j], 128 columns c a
+// workgroup: its 4 waves take tiles in turn, each with sums of its own that
+// meet in LDS.  The contraction runs over rows, across memory: a lane loads 8
+// rows of 8 columns and pairs their halves into the 8 fragments (MFMA t has
+// column 8 i + t as its row i).  v is three bf16 parts, which hold all 24 bits
+// of it, so the gradients are as exact as f32 sums are.
+constexpr int kOuterWaves = 4;
+
+struct Outer {
+    const uint16_t *y;
+    int64_t ldy;
+    const float *v;   // f32 [M, R]
+    float *d;         // split s of d starts at s * L * R * C
+    int C, groups;    // columns; workgroups of 128 columns
+    bool ranks_first; // [R, C] or [C, R]
+};
+struct OuterPair {
+    Outer a, b;       // dA: y = x, v = g; dB: y = dy, v = u
+};
+
+// Eight f32 values as three bf16 parts: the first two are cut (not rounded)
+// off the remainder, so each remainder is exact; an infinity or NaN has none.
+__device__ __forceinline__ void split3(const float *f, v4u (&s)[3]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float a = f[2 * p], b = f[2 * p + 1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float ha = __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), hb = __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
+            s[i][p] = halves(__float_as_uint(a), __float_as_uint(b), true);
+            a = i || __builtin_isfinite(a) ? a - ha : 0.f;
+            b = i || __builtin_isfinite(b) ? b - hb : 0.f;
+        }
+        s[2][p] = pack_bf16x2(a, b);
+    }
+}
+
+template <int JB>
+__global__ __launch_bounds__(64 * kOuterWaves) void lora_outer_kernel(OuterPair both, int64_t M, int L, int R,
+                                                                      const int32_t *ranks, const int32_t *plan, int T,
+                                                                      int splits, int j_parts) {
+    __shared__ float sums[kOuterWaves][8][64];
+    // blocks: dA's, then dB's; of each by adapter, split, part of the rank, columns
+    const int per = L * splits * j_parts;
+    const bool is_a = (int)blockIdx.x < both.a.groups * per;
+    const Outer &o = is_a ? both.a : both.b;
+    int q = is_a ? blockIdx.x : blockIdx.x - both.a.groups * per;
+    const int col0 = q % o.groups * 128;
+    q /= o.groups;
+    const int j0 = q % j_parts * (16 * JB);
+    q /= j_parts;
+    const int split = q % splits, l = q / splits;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fi = lane & 15, fg = lane >> 4;
+    const int r = rank_of(ranks, l, R);
+    const int32_t *first = plan + 4 * (int64_t)T;
+    const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
+    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits), end = t0 + (int)((int64_t)n * (split + 1) / splits);
+    v4f acc[8][JB];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int b = 0; b < JB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    if (j0 < r) {
+        for (int i = begin + wave; i < end; i += kOuterWaves) {
+            const Tile tile = load_tile(plan, i, M, L);
+            const auto ry = rows_rsrc(o.y, tile.row0, tile.rows, o.ldy, o.C);
+            const auto rv = v_rsrc(o.v, tile.row0, tile.rows, R);
+            for (int m0 = 0; m0 < tile.rows; m0 += 32) {
+                // rows past the tile read 0 in both; columns past C are not stored
+                v4u d[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) d[k] = load16(ry, (int)((m0 + 8 * fg + k) * o.ldy + col0 + 8 * fi) * 2);
+                float f[JB][8];
+#pragma unroll
+                for (int b = 0; b < JB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        f[b][k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                            rv, ((m0 + 8 * fg + k) * R + j0 + b * 16 + fi) * 4, 0, 0));
+                v4u yf[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) yf[t][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
+#pragma unroll
+                for (int b = 0; b < JB; ++b) {
+                    v4u s[3];
+                    split3(f[b], s);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) acc[t][b] = mfma(yf[t], s[k], acc[t][b]);
+                }
+            }
+        }
+    }
+    // lane's (t, b, e): column 8 (4 fg + e) + t, rank 16 b + fi
+    float *d = o.d + ((int64_t)split * L + l) * R * o.C;
+#pragma unroll
+    for (int b = 0; b < JB; ++b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < 8; ++t) sums[wave][t][lane] = acc[t][b][e];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 512; i += 64 * kOuterWaves) {
+                // consecutive threads along the contiguous index of d
+                const int t = o.ranks_first ? i & 7 : i >> 6, g = o.ranks_first ? i >> 3 & 3 : i >> 4 & 3;
+                const int jj = o.ranks_first ? i >> 5 : i & 15;
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < kOuterWaves; ++k) s += sums[k][t][g * 16 + jj];
+                const int c = col0 + 8 * (4 * g + e) + t, j = j0 + b * 16 + jj;
+                if (c < o.C && j < R) d[o.ranks_first ? (int64_t)j * o.C + c : (int64_t)c * R + j] = j < r ? s : 0.f;
+            }
+        }
+    }
+}
+
+// da = sum of its splits [splits][na], db likewise (na, nb multiples of 4).
+__global__ __launch_bounds__(256) void lora_reduce_kernel(const float *pa, int64_t na, float *da, const float *pb,
+                                                          int64_t nb, float *db, int splits) {
+    int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const float *p = pa;
+    float *d = da;
+    int64_t n = na;
+    if (i >= na) i -= na, p = pb, d = db, n = nb;
+    if (i >= n) return;
+    v4f s = *reinterpret_cast<const v4f *>(p + i);
+    for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const v4f *>(p + k * n + i);
+    *reinterpret_cast<v4f *>(d + i) = s;
+}
+
+// ---------------------------------------------------------------- host side
+int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
+// v [M, R] = scale x w^T, w [L, R, C] or, TR, [L, C, R].
+template <bool TR>
+void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uint16_t *w, int64_t L, int64_t R,
+                 const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T, float *v, hipStream_t stream) {
+    // 32 rows a workgroup read the weights half as often; 16 where that would leave CUs idle
+    const bool two = 2 * T >= 256;
+    const int grid = (int)(two ? 2 * T : 4 * T);
+#define W8A8_DOWN(JB, RB)                                                                                          \
+    lora_down_kernel<JB, RB, TR><<<grid, 64 * kDownWaves, 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, \
+                                                                       ranks, plan, v)
+    switch (rank_blocks(R)) {
+    case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
+    case 2: two ? W8A8_DOWN(2, 2) : W8A8_DOWN(2, 1); break;
+    case 4: two ? W8A8_DOWN(4, 2) : W8A8_DOWN(4, 1); break;
+    default: two ? W8A8_DOWN(8, 2) : W8A8_DOWN(8, 1); break;
+    }
+#undef W8A8_DOWN
+}
+
+template <bool TR>
+void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t L, int64_t R, const int32_t *ranks,
+               const int32_t *plan, int64_t T, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout,
+               hipStream_t stream) {
+    const int groups = (int)((C + 128 * kUpWaves - 1) / (128 * kUpWaves));
+#define W8A8_UP(JB)                                                                                                  \
+    lora_up_kernel<JB, TR><<<(int)(T * groups), 64 * kUpWaves, 0, stream>>>(v, w, M, (int)C, (int)L, (int)R, ranks,   \
+                                                                            plan, groups, base, ldbase, out, ldout)
+    switch (rank_blocks(R)) {
+    case 1: W8A8_UP(1); break;
+    case 2: W8A8_UP(2); break;
+    case 4: W8A8_UP(4); break;
+    default: W8A8_UP(8); break;
+    }
+#undef W8A8_UP
+}
+
+// Over how many workgroups an adapter's rows are split: enough of them for
+// the chip, each with a tile for every wave.
+int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
+    const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L * (R > 64 ? 2 : 1);
+    int64_t s = (1024 + one - 1) / one;
+    if (s > (T + kOuterWaves - 1) / kOuterWaves) s = (T + kOuterWaves - 1) / kOuterWaves;
+    return s < 1 ? 1 : s;
 }
 
 constexpr int64_t kMaxWidth = 1 << 22;
@@ -108,14 +489,13 @@ bool bad_width(int64_t w) { return w < 8 || w % 8 != 0 || w > kMaxWidth; }
 bool bad_stride(int64_t ld, int64_t w) { return ld < w || ld % 8 != 0 || ld > kMaxWidth; }
 
 w8a8_status lora_check(int64_t M, int64_t K, int64_t N, int64_t R, int64_t L, int64_t T, const uint16_t *a,
-                       const uint16_t *b, const float *scale, const int32_t *ranks, const int32_t *plan,
-                       const void *workspace) {
+                       const uint16_t *b, const float *scale, const int32_t *ranks, const int32_t *plan) {
     if (M < 0 || T < 0 || L < 1 || R < 8 || R > kMaxR) return W8A8_ERR_INVALID_ARG;
-    if (R % 8 != 0 || bad_width(K) || bad_width(N) || L > kMaxL || M > (1 << 30) || T > (1 << 24))
+    if (R % 8 != 0 || bad_width(K) || bad_width(N) || L > kMaxL || M > (1 << 30) || T > (1 << 24) ||
+        T * ((K > N ? K : N) / 512 + 1) > INT32_MAX)
         return W8A8_ERR_SHAPE;
-    if (!a || !b || !plan || !workspace) return W8A8_ERR_INVALID_ARG;
-    if (!aligned16(a) || !aligned16(b) || !aligned16(scale) || !aligned16(ranks) || !aligned16(plan) ||
-        !aligned16(workspace))
+    if (!a || !b || !plan) return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(scale) || !aligned16(ranks) || !aligned16(plan))
         return W8A8_ERR_ALIGN;
     return W8A8_OK;
 }
@@ -167,9 +547,9 @@ extern "C" w8a8_status lora_plan(const int64_t *lengths, const int32_t *adapters
     return W8A8_OK;
 }
 
-extern "C" size_t lora_forward_workspace_bytes(int64_t T, int64_t K, int64_t R) {
-    if (T < 0 || K < 8 || R < 8 || R > w8a8::kMaxR) return 0;
-    return (size_t)T * w8a8::kTileRows * R * sizeof(float);
+extern "C" size_t lora_forward_workspace_bytes(int64_t M, int64_t R) {
+    if (M < 0 || R < 8 || R > w8a8::kMaxR) return 0;
+    return (size_t)(M * R) * sizeof(float);
 }
 
 extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint16_t *a,
@@ -179,21 +559,23 @@ extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int
                                     hipStream_t stream) {
     using namespace w8a8;
     if (M == 0 || T == 0) return M < 0 || T < 0 ? W8A8_ERR_INVALID_ARG : W8A8_OK;
-    const w8a8_status st = lora_check(M, K, N, R, L, T, a, b, scale, ranks, plan, workspace);
+    const w8a8_status st = lora_check(M, K, N, R, L, T, a, b, scale, ranks, plan);
     if (st != W8A8_OK) return st;
     if (bad_stride(ldx, K) || bad_stride(ldout, N) || (base && bad_stride(ldbase, N))) return W8A8_ERR_SHAPE;
-    if (!x || !out) return W8A8_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(u)) return W8A8_ERR_ALIGN;
-    float *p = static_cast<float *>(workspace);
-    lora_down_kernel<<<(int)T, kThreads, 0, stream>>>(x, M, (int)K, ldx, a, R * K, K, 1, (int)L, (int)R, scale, ranks, plan, p, u);
-    const dim3 grid((unsigned)T, (unsigned)((N + kThreads - 1) / kThreads));
-    lora_up_kernel<<<grid, kThreads, 0, stream>>>(p, b, N * R, 1, R, M, (int)N, (int)L, (int)R, ranks, plan, base, ldbase, out, ldout);
+    if (!x || !out || (!u && !workspace)) return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(u) || !aligned16(workspace))
+        return W8A8_ERR_ALIGN;
+    float *v = u ? u : static_cast<float *>(workspace);
+    down_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, stream);
+    up_launch<false>(v, b, M, N, L, R, ranks, plan, T, base, ldbase, out, ldout, stream);
     return launch_status();
 }
 
-extern "C" size_t lora_backward_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
-    if (T < 0 || K < 8 || N < 8 || L < 1 || R < 8 || R > w8a8::kMaxR) return 0;
-    return (size_t)(T * w8a8::kTileRows * R * sizeof(float) + 16);
+extern "C" size_t lora_backward_workspace_bytes(int64_t M, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
+    using namespace w8a8;
+    if (M < 0 || T < 0 || K < 8 || N < 8 || L < 1 || R < 8 || R > kMaxR) return 0;
+    const int64_t splits = outer_splits(T, K, N, R, L);
+    return (size_t)(M * R + (splits > 1 ? splits * L * R * (K + N) : 0)) * sizeof(float);
 }
 
 extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, int64_t lddy, const uint16_t *x,
@@ -203,29 +585,41 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
                                      uint16_t *dx, int64_t lddx, float *da, float *db, void *workspace,
                                      hipStream_t stream) {
     using namespace w8a8;
-    const w8a8_status st = lora_check(M, K, N, R, L, T, a, b, scale, ranks, plan, workspace);
+    const w8a8_status st = lora_check(M, K, N, R, L, T, a, b, scale, ranks, plan);
     if (st != W8A8_OK) return st;
     if (bad_stride(ldx, K) || bad_stride(lddy, N) || (dx && bad_stride(lddx, K)) || (base && bad_stride(ldbase, K)))
         return W8A8_ERR_SHAPE;
-    if (M > 0 && T > 0 && (!dy || (da && !x) || (db && !u))) return W8A8_ERR_INVALID_ARG;
+    if (M == 0) T = 0;
+    if (T > 0 && (!dy || (da && !x) || (db && !u) || !workspace)) return W8A8_ERR_INVALID_ARG;
     if ((da == nullptr) != (db == nullptr)) return W8A8_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(x) || !aligned16(u) || !aligned16(base) || !aligned16(dx) || !aligned16(da) ||
-        !aligned16(db))
+        !aligned16(db) || !aligned16(workspace))
         return W8A8_ERR_ALIGN;
-    if (M == 0) T = 0;
-    float *p = static_cast<float *>(workspace);
+    float *g = static_cast<float *>(workspace), *parts = g + M * R;
     if (T > 0) {
-        lora_down_kernel<<<(int)T, kThreads, 0, stream>>>(dy, M, (int)N, lddy, b, N * R, 1, R, (int)L, (int)R, scale, ranks, plan, p, nullptr);
-        if (dx) {
-            const dim3 grid((unsigned)T, (unsigned)((K + kThreads - 1) / kThreads));
-            lora_up_kernel<<<grid, kThreads, 0, stream>>>(p, a, R * K, K, 1, M, (int)K, (int)L, (int)R, ranks, plan, base, ldbase, dx, lddx);
-        }
+        down_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, stream);
+        if (dx) up_launch<true>(g, a, M, K, L, R, ranks, plan, T, base, ldbase, dx, lddx, stream);
     }
     if (da) {
-        const dim3 ga((unsigned)((K + kThreads - 1) / kThreads), (unsigned)R, (unsigned)L);
-        lora_outer_kernel<<<ga, kThreads, 0, stream>>>(nullptr, p, x, M, (int)K, ldx, (int)L, (int)R, ranks, plan, (int)T, K, 1, da);
-        const dim3 gb((unsigned)((N + kThreads - 1) / kThreads), (unsigned)R, (unsigned)L);
-        lora_outer_kernel<<<gb, kThreads, 0, stream>>>(u, nullptr, dy, M, (int)N, lddy, (int)L, (int)R, ranks, plan, (int)T, 1, R, db);
+        const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
+        const int j_parts = R > 64 ? 2 : 1;
+        const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
+        const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga, true},
+                                {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb, false}};
+        const int64_t grid = (ga + gb) * L * splits * j_parts;
+        if (grid > INT32_MAX) return W8A8_ERR_SHAPE;
+#define W8A8_OUTER(JB)                                                                                        \
+    lora_outer_kernel<JB><<<(int)grid, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan,   \
+                                                                     (int)T, (int)splits, j_parts)
+        switch (rank_blocks(R)) {
+        case 1: W8A8_OUTER(1); break;
+        case 2: W8A8_OUTER(2); break;
+        default: W8A8_OUTER(4); break;
+        }
+#undef W8A8_OUTER
+        if (splits > 1)
+            lora_reduce_kernel<<<(int)(((na + nb) / 4 + 255) / 256), 256, 0, stream>>>(parts, na, da, parts + splits * na, nb,
+                                                                                      db, (int)splits);
     }
     return launch_status();
 }
