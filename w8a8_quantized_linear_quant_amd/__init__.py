@@ -127,8 +127,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a torch.cuda.Stream (0.1 us against 2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _qtype_of(codes):
@@ -467,7 +473,7 @@ def gguf_a8_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
 
 
 # ------------------------------------------------------------------ adapters
-def _view(t, shape, dtype, device, name, align=True):
+def _view(t, rows, cols, dtype, device, name, align=True):
     """A matrix operand that may be a view with a row stride, never copied:
     (data pointer, row stride in elements).  `align`: rows must start on
     16-byte boundaries."""
@@ -477,28 +483,28 @@ def _view(t, shape, dtype, device, name, align=True):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if rows > 1 else cols
-    ptr = t.data_ptr()
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    ptr, ld = t.data_ptr(), cols
+    if not t.is_contiguous():
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        ld = t.stride(0) if rows > 1 else cols
+        if ld < cols:
+            raise ValueError(f"{name}'s rows overlap (row stride {ld} < {cols})")
     if rows > 0 and (ptr % 16 != 0 or (align and ld % 8 != 0)):
         raise ValueError(f"{name} must start on a 16-byte boundary" +
                          (f", its rows too (row stride {ld} must be a multiple of 8)" if align else ""))
-    if rows > 1 and ld < cols:
-        raise ValueError(f"{name}'s rows overlap (row stride {ld} < {cols})")
     return ptr, ld
 
 
 def _vec(t, n, dtype, device, name):
-    """A contiguous vector operand of at least n elements, or None: its pointer."""
+    """A contiguous operand of at least n elements, or None: its pointer."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device != device or not t.is_contiguous() or t.numel() < n:
+    if t.device != device or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, on {device}, of at least {n} elements")
     return t.data_ptr()
 
@@ -573,11 +579,11 @@ def lora_forward(x, a, b, plan, scale=None, ranks=None, base=None, out=None, u=N
     dev = _gpu_matrix(x, "x")
     M = x.shape[0]
     L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
-    px, ldx = _view(x, (M, K), torch.bfloat16, dev, "x")
-    pbase, ldbase = (None, 0) if base is None else _view(base, (M, N), torch.bfloat16, dev, "base")
+    px, ldx = _view(x, M, K, torch.bfloat16, dev, "x")
+    pbase, ldbase = (None, 0) if base is None else _view(base, M, N, torch.bfloat16, dev, "base")
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    po, ldo = _view(out, (M, N), torch.bfloat16, dev, "out")
+    po, ldo = _view(out, M, N, torch.bfloat16, dev, "out")
     if u is None and save_u:
         u = torch.empty((M, R), dtype=torch.float32, device=dev)
     pu = None if u is None else _vec(u, M * R, torch.float32, dev, "u")
@@ -598,14 +604,14 @@ def lora_backward(dy, x, u, a, b, plan, scale=None, ranks=None, base=None, out=N
     dev = _gpu_matrix(dy, "dy")
     M = dy.shape[0]
     L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
-    pdy, lddy = _view(dy, (M, N), torch.bfloat16, dev, "dy")
-    px, ldx = _view(x, (M, K), torch.bfloat16, dev, "x")
+    pdy, lddy = _view(dy, M, N, torch.bfloat16, dev, "dy")
+    px, ldx = _view(x, M, K, torch.bfloat16, dev, "x")
     pu = _vec(u, M * R, torch.float32, dev, "u")
-    pbase, ldbase = (None, 0) if base is None else _view(base, (M, K), torch.bfloat16, dev, "base")
+    pbase, ldbase = (None, 0) if base is None else _view(base, M, K, torch.bfloat16, dev, "base")
     dx, pdx, lddx = None, None, 0
     if need_dx:
         dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if out is None else out
-        pdx, lddx = _view(dx, (M, K), torch.bfloat16, dev, "out")
+        pdx, lddx = _view(dx, M, K, torch.bfloat16, dev, "out")
     if need_weights:
         if u is None:
             raise ValueError("u, as lora_forward returned it, is needed for the weights' gradients")
@@ -636,25 +642,33 @@ def _norm_args(x, weight, bias):
     dev = _gpu_matrix(x, "x")
     M, K = x.shape
     xt = _dtype_of(x, "x")
-    px, ldx = _view(x, (M, K), x.dtype, dev, "x", align=False)
+    px, ldx = _view(x, M, K, x.dtype, dev, "x", align=False)
     p = weight if weight is not None else bias
-    wt = xt if p is None else _dtype_of(p, "weight")
-    pw = None if weight is None else _vec(weight, K, weight.dtype, dev, "weight")
-    pb = None if bias is None else _vec(bias, K, weight.dtype if weight is not None else bias.dtype, dev, "bias")
+    if p is None:
+        return dev, M, K, xt, px, ldx, xt, None, None
+    wt = _dtype_of(p, "weight")
+    pw, pb = _vec(weight, K, p.dtype, dev, "weight"), _vec(bias, K, p.dtype, dev, "bias")
     return dev, M, K, xt, px, ldx, wt, pw, pb
+
+
+def _first(t, n):
+    return t if t.numel() == n else t[:n]
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
     """x bf16 or f32 [M, K] (may have a row stride, of any alignment); weight, bias [K] of one dtype (bf16 or f32)
     or None.  Returns (y like x, mean f32 [M], rstd f32 [M])."""
     dev, M, K, xt, px, ldx, wt, pw, pb = _norm_args(x, weight, bias)
-    y = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else out
-    py, ldy = _view(y, (M, K), x.dtype, dev, "out", align=False)
-    mean = _buf(mean, M, torch.float32, dev, "mean")
-    rstd = _buf(rstd, M, torch.float32, dev, "rstd")
-    _check(_lib.layer_norm_forward(xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, mean.data_ptr(), rstd.data_ptr(),
-                                   _stream(dev)))
-    return y, mean[:M], rstd[:M]
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=dev)
+    py, ldy = _view(out, M, K, x.dtype, dev, "out", align=False)
+    if mean is None:
+        mean = torch.empty(M, dtype=torch.float32, device=dev)
+    if rstd is None:
+        rstd = torch.empty_like(mean)
+    pm, pr = _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd")
+    _check(_lib.layer_norm_forward(xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, pm, pr, _stream(dev)))
+    return out, _first(mean, M), _first(rstd, M)
 
 
 def layer_norm_backward_workspace_bytes(M, K):
@@ -666,12 +680,12 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, dweight=None, 
     """Gradients of layer_norm_forward from its x, mean, rstd and weight.  Returns (dx like x, dweight f32 [K],
     dbias f32 [K]), None for what is not needed (need_params: default, if there is a weight)."""
     dev, M, K, xt, px, ldx, wt, pw, _ = _norm_args(x, weight, None)
-    pdy, lddy = _view(dy, (M, K), x.dtype, dev, "dy", align=False)
+    pdy, lddy = _view(dy, M, K, x.dtype, dev, "dy", align=False)
     pm, pr = _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd")
     dx, pdx, lddx = None, None, 0
     if need_dx:
         dx = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else out
-        pdx, lddx = _view(dx, (M, K), x.dtype, dev, "out", align=False)
+        pdx, lddx = _view(dx, M, K, x.dtype, dev, "out", align=False)
     if weight is not None if need_params is None else need_params:
         dweight = _out(dweight, (K,), torch.float32, dev, "dweight")
         dbias = _out(dbias, (K,), torch.float32, dev, "dbias")
@@ -692,11 +706,12 @@ def w8a8_quant_act_rowwise_layer_norm(x, weight=None, bias=None, eps=1e-5, qtype
     dev, M, K, xt, px, ldx, wt, pw, pb = _norm_args(x, weight, bias)
     ldq = ldq if ldq is not None else K + (-K) % 16
     xq = _out(out, (M, ldq), cd, dev, "out")
-    s = _buf(scale, M, torch.float32, dev, "scale")
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
     _check(_lib.w8a8_quant_act_rowwise_layer_norm(
-        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, s.data_ptr(),
+        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, _vec(scale, M, torch.float32, dev, "scale"),
         _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd"), _stream(dev)))
-    return xq, s[:M]
+    return xq, _first(scale, M)
 
 
 # ---------------------------------------------------------------- diagnostics

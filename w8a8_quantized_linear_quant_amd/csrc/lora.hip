@@ -63,96 +63,142 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
 // 8 (lane / 16) .. + 7; D row 4 (lane / 16) + e, column lane % 16.
 
 // ---------------------------------------------------------------- down
-// One workgroup takes 16 RB rows of a tile over all of C: 16 waves split the
-// 32-wide steps of the contraction (pairs of steps, so that a wave reads whole
-// 128-byte lines), U steps' loads in flight at a time, and their sums meet in
-// LDS.  No partial sums leave the workgroup.  JB: 16-wide blocks of the rank.
-constexpr int kDownWaves = 16;
+// One workgroup takes 16 RB rows of a tile over all of C; its waves take
+// 128-wide slices of the contraction in turn and their sums meet in LDS, so
+// that no partial sums leave the workgroup.  JB: 16-wide blocks of the rank.
+//
+// A fragment wants 16 rows in 16 consecutive lanes, which from memory would be
+// 64 separate 16-byte requests a load (85 cycles of a CU's address unit where
+// 16 do: 38 us at M 8192, C 4096, R 64).  So x and the weight are loaded with
+// 16 lanes along a row (256 bytes) and turned in a 4 KB piece of LDS of the
+// wave's own: a block is written there, its registers are loaded again at once
+// with the next one's data, and its fragments are read back.  LDS accesses of
+// a wave stay in order, so no barrier is needed.
+constexpr int kSlice = 128;
+// 16 waves where 128 registers hold a wave's sums and its blocks in flight.
+constexpr int down_waves(int JB, int RB) { return RB == 1 && JB <= 4 ? 16 : 8; }
 
-// TR's weight fragments: 32 rows n of B by 16 JB ranks go through a wave's own
-// piece of LDS and come back transposed (ds_read_b64_tr_b16: each 16 lanes
-// read 4 rows of 16 columns, lane i receives column i's 4 values).
-template <int JB>
-__device__ __forceinline__ void stage_transposed(uint16_t *area, const v4u (&d)[JB], int lane) {
+// Block of 16 rows x 256 bytes: chunk c of row i in slot c ^ i, so that 16
+// rows' reads of one chunk fall on distinct banks.
+__device__ __forceinline__ void turn_in(char *area, const v4u (&d)[4], int lane) {
 #pragma unroll
-    for (int i = 0; i < JB; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 8) = d[i];
+    for (int i = 0; i < 4; ++i) {
+        const int row = i * 4 + (lane >> 4), c = lane & 15;
+        *reinterpret_cast<v4u *>(area + row * 256 + ((c ^ row) << 4)) = d[i];
+    }
 }
+__device__ __forceinline__ v4u turn_out(const char *area, int step, int lane) {
+    const int row = lane & 15, c = step * 4 + (lane >> 4);
+    return *reinterpret_cast<const v4u *>(area + row * 256 + ((c ^ row) << 4));
+}
+
+// TR's weight fragments: 32 rows n of B by 16 JB ranks, written as they lie,
+// read transposed (ds_read_b64_tr_b16: each 16 lanes read 4 rows of 16
+// columns, lane i receives column i's 4 values).
 template <int JB>
-__device__ __forceinline__ v4u transposed_fragment(uint16_t *area, int jb, int lane) {
+__device__ __forceinline__ v4u transposed_fragment(const char *area, int jb, int lane) {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s lds_v4s;
     const int g = lane >> 4, q = lane & 15;
-    uint16_t *p = area + (8 * g + q / 4) * (16 * JB) + jb * 16 + (q % 4) * 4;
+    const char *p = area + (8 * g + q / 4) * (32 * JB) + jb * 32 + (q % 4) * 8;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * 16 * JB));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * 32 * JB));
     const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
     return v4u{a.x, a.y, b.x, b.y};
 }
 
 template <int JB, int RB, bool TR>
-__global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
+__global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
                                                                     const uint16_t *w, int L, int R,
                                                                     const float *scale, const int32_t *ranks,
                                                                     const int32_t *plan, float *v) {
-    constexpr int U = JB * RB <= 2 ? 4 : JB <= 4 ? 2 : 1;
-    constexpr int kStage = TR ? kDownWaves * U * JB * 512 * 2 : 0;            // bytes
-    constexpr int kSums = kDownWaves * RB * 16 * 17 * 4;
-    __shared__ __attribute__((aligned(16))) char lds[kStage > kSums ? kStage : kSums];
+    constexpr int W = down_waves(JB, RB);
+    constexpr int kArea = TR && JB > 4 ? JB * 1024 : 4096;  // bytes of a wave
+    constexpr int kSums = W * RB * 16 * 17 * 4;
+    __shared__ __attribute__((aligned(16))) char lds[W * kArea > kSums ? W * kArea : kSums];
     constexpr int kParts = 4 / RB;
     const Tile tile = load_tile(plan, blockIdx.x / kParts, M, L);
     const int first = (blockIdx.x % kParts) * (16 * RB);
     if (first >= tile.rows) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = rank_of(ranks, tile.adapter, R);
+    const float s = tile.adapter >= 0 && scale ? scale[tile.adapter] : 1.f;
     v4f acc[RB][JB];
 #pragma unroll
     for (int a = 0; a < RB; ++a)
 #pragma unroll
         for (int b = 0; b < JB; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if (r > 0) {  // the same for the whole workgroup
+    const int slices = (C + kSlice - 1) / kSlice;
+    if (r > 0 && wave < slices) {  // r: the same for the whole workgroup
         const auto rx = rows_rsrc(x, tile.row0 + first, tile.rows - first, ldx, C);
         const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)tile.adapter * R * C, (short)0,
                                                           R * C * 2, kBufferRsrcWord3);
-        const int fi = lane & 15, fg = lane >> 4;
-        uint16_t *area = reinterpret_cast<uint16_t *>(lds) + wave * (U * JB * 512);
-        const int steps = (C + 31) / 32;
-        // this wave's n-th step: 2 wave + (n & 1) + 32 (n / 2)
-        for (int n = 0; 2 * wave + 16 * (n & ~1) < steps; n += U) {
-            v4u xf[U][RB], wf[U][JB];
+        char *area = lds + wave * kArea;
+        const int li = lane >> 4, lc = (lane & 15) * 8;  // row and column of a lane in a load of 4 rows x 128
+        // past C both factors read 0: neither may be whatever lies behind a row
+        auto fetch_x = [&](int slice, int a, v4u (&d)[4]) {
+            const int k = slice * kSlice + lc;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int s = U == 1 ? 2 * wave + (n & 1) + (n & ~1) * 16 : 2 * wave + (i & 1) + (n + (i & ~1)) * 16;
-                const int k = s * 32 + fg * 8;
-                // past C both factors read 0: neither may be whatever lies behind a row
+            for (int i = 0; i < 4; ++i)
+                d[i] = load16(rx, k < C ? (int)((a * 16 + i * 4 + li) * ldx + k) * 2 : kOobOffset);
+        };
+        constexpr int kUnits = TR ? 4 : JB, kUnit = TR ? JB : 4;  // weight blocks of a slice, loads of a block
+        auto fetch_w = [&](int slice, int unit, v4u (&d)[kUnit]) {
 #pragma unroll
-                for (int a = 0; a < RB; ++a)
-                    xf[i][a] = load16(rx, k < C ? (int)((a * 16 + fi) * ldx + k) * 2 : kOobOffset);
-#pragma unroll
-                for (int b = 0; b < JB; ++b) {
-                    if constexpr (TR) {
-                        const int c = b * 64 + lane, row = s * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
-                        wf[i][b] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
-                    } else {
-                        wf[i][b] = load16(rw, k < C ? ((b * 16 + fi) * C + k) * 2 : kOobOffset);
-                    }
+            for (int i = 0; i < kUnit; ++i) {
+                if constexpr (TR) {  // 32 rows n of a step, all ranks
+                    const int c = i * 64 + lane, row = slice * kSlice + unit * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
+                    d[i] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
+                } else {             // 16 ranks of a slice
+                    const int k = slice * kSlice + lc;
+                    d[i] = load16(rw, k < C ? ((unit * 16 + i * 4 + li) * C + k) * 2 : kOobOffset);
                 }
             }
-            if constexpr (TR) {
+        };
+        // Workgroups start at different slices: in step, they would all read
+        // the same few kilobytes of every row (with rows a power of two apart
+        // a quarter of the memory channels) and the same lines of the weight
+        // (8 XCDs: blocks 8 apart share an L2).
+        const int turns = (slices + W - 1) / W;
+        int turn = (int)((blockIdx.x / 8 + blockIdx.x) % (unsigned)turns);
+        v4u xd[RB][4], wd[kUnit];
+        int slice = turn * W + wave;
 #pragma unroll
-                for (int i = 0; i < U; ++i) stage_transposed<JB>(area + i * JB * 512, wf[i], lane);
+        for (int a = 0; a < RB; ++a) fetch_x(slice, a, xd[a]);
+        fetch_w(slice, 0, wd);
+        for (int n = 0; n < turns; ++n) {  // a slice past the end reads 0 without touching memory
+            turn = turn + 1 < turns ? turn + 1 : 0;
+            const int next = n + 1 < turns ? turn * W + wave : slices;
+            v4u xf[RB][4];
+#pragma unroll
+            for (int a = 0; a < RB; ++a) {
+                turn_in(area, xd[a], lane);
+                fetch_x(next, a, xd[a]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) xf[a][t] = turn_out(area, t, lane);
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+            for (int q = 0; q < kUnits; ++q) {
+                if constexpr (TR) {
 #pragma unroll
-                for (int b = 0; b < JB; ++b) {
-                    const v4u f = TR ? transposed_fragment<JB>(area + i * JB * 512, b, lane) : wf[i][b];
-#pragma unroll
-                    for (int a = 0; a < RB; ++a) acc[a][b] = mfma(xf[i][a], f, acc[a][b]);
+                    for (int i = 0; i < kUnit; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 16) = wd[i];
+                } else {
+                    turn_in(area, wd, lane);
                 }
+                if (q + 1 < kUnits) fetch_w(slice, q + 1, wd);
+                else fetch_w(next, 0, wd);
+#pragma unroll
+                for (int i = 0; i < (TR ? JB : 4); ++i) {
+                    const v4u f = TR ? transposed_fragment<JB>(area, i, lane) : turn_out(area, i, lane);
+                    const int t = TR ? q : i, b = TR ? i : q;
+#pragma unroll
+                    for (int a = 0; a < RB; ++a) acc[a][b] = mfma(xf[a][t], f, acc[a][b]);
+                }
+            }
+            slice = next;
         }
     }
-    const float s = tile.adapter >= 0 && scale ? scale[tile.adapter] : 1.f;
     auto part = reinterpret_cast<float (*)[RB * 16][17]>(lds);
 #pragma unroll
     for (int b = 0; b < JB; ++b) {
@@ -166,29 +212,33 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(const uint16
         if (row < RB * 16 && first + row < tile.rows && j < R) {
             float t = 0.f;
 #pragma unroll
-            for (int k = 0; k < kDownWaves; ++k) t += part[k][row][threadIdx.x % 16];
+            for (int k = 0; k < W; ++k) t += part[k][row][threadIdx.x % 16];
             v[(tile.row0 + first + row) * R + j] = j < r ? t * s : 0.f;
         }
     }
 }
 
 // ------------------------------------------------------------------ up
-// D^T = W v^T: the MFMA's rows are columns of the output, its columns the
-// tile's rows, so that a lane holds 8 consecutive columns of one row and base
-// and out move as 16-byte accesses.  A wave takes 128 columns (8 MFMAs: MFMA t
-// has column 8 pi(i) + t as its row i, pi(4 g + e) = 4 e + g) of all the
-// tile's rows, with its weights in registers.  v is two bf16 halves (hi + lo,
-// ~16 bits); up to R = 16 both fit one 32-wide contraction, the weight twice.
+// A wave takes 128 columns of all the tile's rows, its weights in registers
+// and all of base in flight at once.  MFMA t of 8 has column 8 i + t as its
+// column i: a lane then holds 8 consecutive columns of a row, 16 lanes 256
+// bytes of it, and base (the sums' start) and out move as 16-byte accesses.
+// (The transposed product, 16 rows in 16 consecutive lanes, makes 64 requests
+// of each access: 99 us against %UP% at M 8192, C 12288, R 64.)  The workgroup
+// turns v into two bf16 halves (hi + lo, ~16 bits) in LDS; up to R = 16 both
+// fit one 32-wide contraction, the weight twice.
 constexpr int kUpWaves = 4;
 
-// Eight f32 values as bf16 halves; lo = 0 beside an infinite hi.
-__device__ __forceinline__ void split2(const float *f, v4u &hi, v4u &lo) {
+// Four f32 values as bf16 halves; lo = 0 beside an infinite hi.
+__device__ __forceinline__ void split2(v4f f, uint2 &hi, uint2 &lo) {
+    uint32_t h[2], l[2];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        hi[p] = pack_bf16x2(f[2 * p], f[2 * p + 1]);
-        const float a = __uint_as_float(hi[p] << 16), b = __uint_as_float(hi[p] & 0xFFFF0000u);
-        lo[p] = pack_bf16x2(__builtin_isfinite(a) ? f[2 * p] - a : 0.f, __builtin_isfinite(b) ? f[2 * p + 1] - b : 0.f);
+    for (int p = 0; p < 2; ++p) {
+        h[p] = pack_bf16x2(f[2 * p], f[2 * p + 1]);
+        const float a = __uint_as_float(h[p] << 16), b = __uint_as_float(h[p] & 0xFFFF0000u);
+        l[p] = pack_bf16x2(__builtin_isfinite(a) ? f[2 * p] - a : 0.f, __builtin_isfinite(b) ? f[2 * p + 1] - b : 0.f);
     }
+    hi = make_uint2(h[0], h[1]), lo = make_uint2(l[0], l[1]);
 }
 
 // The 16-bit halves of (a, b): the low ones, or the high ones.
@@ -203,44 +253,71 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
                                                                 int64_t ldbase, uint16_t *out, int64_t ldout) {
     constexpr int KB = JB == 1 ? 1 : JB / 2;  // 32-wide contractions
     constexpr int RB = kTileRows / 16;
+    constexpr int P = JB * 16 + 8;  // halves of an LDS row: 16 rows' reads fall on distinct banks
+    __shared__ __attribute__((aligned(16))) uint16_t vs[2][kTileRows][P];
+    __shared__ __attribute__((aligned(16))) char ws[TR ? 1 : kUpWaves][TR ? 16 : JB == 1 ? 4096 : 8192];
     const Tile tile = load_tile(plan, blockIdx.x / groups, M, L);
+    if (tile.rows == 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col0 = (blockIdx.x % groups * kUpWaves + wave) * 128;
-    if (tile.rows == 0 || col0 >= C) return;
+    const auto rv = v_rsrc(v, tile.row0, tile.rows, R);
+    constexpr int kChunks = kTileRows * JB * 4 / (64 * kUpWaves);  // 4-float chunks of v per thread
+    v4u vd[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int q = i * 64 * kUpWaves + threadIdx.x, row = q / (JB * 4), j = q % (JB * 4) * 4;
+        vd[i] = load16(rv, j < R ? (row * R + j) * 4 : kOobOffset);
+    }
     const int r = rank_of(ranks, tile.adapter, R);
     const int fi = lane & 15, fg = lane >> 4;
     const int jg = JB == 1 ? fg & 1 : fg;  // this lane's 8 ranks of a contraction
 
-    // base, for all the row blocks at once
     v4u bf[RB][4];
     const auto rb = rows_rsrc(base, tile.row0, base ? tile.rows : 0, ldbase, C);
 #pragma unroll
     for (int a = 0; a < RB; ++a) {
         if (a * 16 >= tile.rows) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bf[a][e] = load16(rb, (int)((a * 16 + fi) * ldbase + col0 + 8 * (4 * e + fg)) * 2);
+        for (int e = 0; e < 4; ++e) bf[a][e] = load16(rb, (int)((a * 16 + 4 * fg + e) * ldbase + col0 + 8 * fi) * 2);
     }
     // weight fragments: entries beyond the adapter's rank are 0, whatever lies there
     v4u wf[8][KB];
-    if (r > 0) {
+    if (r > 0 && col0 < C) {
         const uint16_t *wl = w + (int64_t)tile.adapter * R * C;
-        const int ci = col0 + 8 * (4 * (fi & 3) + (fi >> 2));
+        const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, (TR ? r : R) * C * 2, kBufferRsrcWord3);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             const int j = k * 32 + jg * 8;
             if constexpr (TR) {
-                const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, r * C * 2, kBufferRsrcWord3);
+                // 8 ranks of the lane's 8 columns, paired into the 8 fragments
+                const int c = col0 + 8 * fi;
                 v4u d[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = load16(rw, ci < C ? ((j + i) * C + ci) * 2 : kOobOffset);
+                for (int i = 0; i < 8; ++i) d[i] = load16(rw, c < C ? ((j + i) * C + c) * 2 : kOobOffset);
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) wf[t][k][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
             } else {
-                const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, R * C * 2, kBufferRsrcWord3);
+                // 128 rows of the contraction's kCh chunks of 8 ranks through the
+                // wave's own LDS, slots swizzled for the reads 8 rows apart
+                constexpr int kCh = JB == 1 ? 2 : 4;
+                v4u d[2 * kCh];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) wf[t][k] = load16(rw, ci + t < C && j < R ? ((ci + t) * R + j) * 2 : kOobOffset);
+                for (int i = 0; i < 2 * kCh; ++i) {
+                    const int q = i * 64 + lane, n = q / kCh, jc = k * 32 + q % kCh * 8;
+                    d[i] = load16(rw, col0 + n < C && jc < R ? ((col0 + n) * R + jc) * 2 : kOobOffset);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * kCh; ++i) {
+                    const int q = i * 64 + lane, n = q / kCh;
+                    *reinterpret_cast<v4u *>(ws[wave] + ((q ^ (n >> 3 & 7)) << 4)) = d[i];
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const int q = (8 * fi + t) * kCh + jg;
+                    wf[t][k] = *reinterpret_cast<const v4u *>(ws[wave] + ((q ^ (fi & 7)) << 4));
+                }
                 if (r < R) {
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
@@ -252,7 +329,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
             }
         }
     }
-    const auto rv = v_rsrc(v, tile.row0, tile.rows, R);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int q = i * 64 * kUpWaves + threadIdx.x, row = q / (JB * 4), j = q % (JB * 4) * 4;
+        uint2 hi, lo;
+        split2(__builtin_bit_cast(v4f, vd[i]), hi, lo);
+        *reinterpret_cast<uint2 *>(&vs[0][row][j]) = hi;
+        *reinterpret_cast<uint2 *>(&vs[1][row][j]) = lo;
+    }
+    __syncthreads();
+    if (col0 >= C) return;
 #pragma unroll
     for (int a = 0; a < RB; ++a) {
         if (a * 16 >= tile.rows) break;
@@ -265,36 +351,23 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
         if (r > 0) {
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
-                const int j = k * 32 + jg * 8, at = j < R ? ((a * 16 + fi) * R + j) * 4 : kOobOffset;
-                const v4u d0 = load16(rv, at), d1 = load16(rv, at + 16);
-                float f[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(d0[i]), f[4 + i] = __uint_as_float(d1[i]);
-                v4u hi, lo;
-                split2(f, hi, lo);
-                if constexpr (JB == 1) {
-                    const v4u h = fg < 2 ? hi : lo;
+                for (int h = 0; h < (JB == 1 ? 1 : 2); ++h) {
+                    const v4u f = *reinterpret_cast<const v4u *>(&vs[JB == 1 ? fg >> 1 : h][a * 16 + fi][k * 32 + jg * 8]);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], h, acc[t]);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], hi, acc[t]);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = mfma(wf[t][k], lo, acc[t]);
+                    for (int t = 0; t < 8; ++t) acc[t] = mfma(f, wf[t][k], acc[t]);
                 }
             }
         }
-        if (a * 16 + fi < tile.rows) {
-            uint16_t *o = out + (tile.row0 + a * 16 + fi) * ldout + col0;
+        const int c = col0 + 8 * fi;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 8 * (4 * e + fg);
-                if (col0 + c >= C) continue;
-                v4u d;
+        for (int e = 0; e < 4; ++e) {
+            const int row = a * 16 + 4 * fg + e;
+            if (row >= tile.rows || c >= C) continue;
+            v4u d;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
-                *reinterpret_cast<v4u *>(o + c) = d;
-            }
+            for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
+            *reinterpret_cast<v4u *>(out + (tile.row0 + row) * ldout + c) = d;
         }
     }
 }
@@ -363,38 +436,51 @@ __global__ __launch_bounds__(64 * kOuterWaves) void lora_outer_kernel(OuterPair 
 #pragma unroll
         for (int b = 0; b < JB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if (j0 < r) {
-        for (int i = begin + wave; i < end; i += kOuterWaves) {
-            const Tile tile = load_tile(plan, i, M, L);
+    if (j0 < r && begin + wave < end) {
+        // 32 rows a step, the next step's loads in flight while one is worked on
+        int i = begin + wave, m0 = 0;
+        Tile tile = load_tile(plan, i, M, L), next = tile;
+        if (i + kOuterWaves < end) next = load_tile(plan, i + kOuterWaves, M, L);
+        v4u d[8];
+        float f[JB][8];
+        auto fetch = [&]() {
+            // rows past the tile read 0 in both; columns past C are not stored
             const auto ry = rows_rsrc(o.y, tile.row0, tile.rows, o.ldy, o.C);
             const auto rv = v_rsrc(o.v, tile.row0, tile.rows, R);
-            for (int m0 = 0; m0 < tile.rows; m0 += 32) {
-                // rows past the tile read 0 in both; columns past C are not stored
-                v4u d[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] = load16(ry, (int)((m0 + 8 * fg + k) * o.ldy + col0 + 8 * fi) * 2);
-                float f[JB][8];
+            for (int k = 0; k < 8; ++k) d[k] = load16(ry, (int)((m0 + 8 * fg + k) * o.ldy + col0 + 8 * fi) * 2);
 #pragma unroll
-                for (int b = 0; b < JB; ++b)
+            for (int b = 0; b < JB; ++b)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        f[b][k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                            rv, ((m0 + 8 * fg + k) * R + j0 + b * 16 + fi) * 4, 0, 0));
-                v4u yf[8];
+                for (int k = 0; k < 8; ++k)
+                    f[b][k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                        rv, ((m0 + 8 * fg + k) * R + j0 + b * 16 + fi) * 4, 0, 0));
+        };
+        fetch();
+        while (true) {
+            v4u yf[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < 8; ++t)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) yf[t][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
+                for (int p = 0; p < 4; ++p) yf[t][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
+            v4u s[JB][3];
 #pragma unroll
-                for (int b = 0; b < JB; ++b) {
-                    v4u s[3];
-                    split3(f[b], s);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) acc[t][b] = mfma(yf[t], s[k], acc[t][b]);
-                }
+            for (int b = 0; b < JB; ++b) split3(f[b], s[b]);
+            m0 += 32;
+            if (m0 >= tile.rows) {
+                i += kOuterWaves, m0 = 0;
+                tile = next;
+                if (i + kOuterWaves < end) next = load_tile(plan, i + kOuterWaves, M, L);
             }
+            const bool more = i < end;
+            if (more) fetch();
+#pragma unroll
+            for (int b = 0; b < JB; ++b)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t][b] = mfma(yf[t], s[b][k], acc[t][b]);
+            if (!more) break;
         }
     }
     // lane's (t, b, e): column 8 (4 fg + e) + t, rank 16 b + fi
@@ -430,8 +516,14 @@ __global__ __launch_bounds__(256) void lora_reduce_kernel(const float *pa, int64
     int64_t n = na;
     if (i >= na) i -= na, p = pb, d = db, n = nb;
     if (i >= n) return;
-    v4f s = *reinterpret_cast<const v4f *>(p + i);
-    for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const v4f *>(p + k * n + i);
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < splits; k += 8) {
+        v4f q[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) q[c] = k + c < splits ? *reinterpret_cast<const v4f *>(p + (k + c) * n + i) : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s += q[c];
+    }
     *reinterpret_cast<v4f *>(d + i) = s;
 }
 
@@ -442,11 +534,12 @@ int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8;
 template <bool TR>
 void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uint16_t *w, int64_t L, int64_t R,
                  const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T, float *v, hipStream_t stream) {
-    // 32 rows a workgroup read the weights half as often; 16 where that would leave CUs idle
+    // 32 rows a workgroup read the weights half as often; 16 where that would
+    // leave CUs idle
     const bool two = 2 * T >= 256;
     const int grid = (int)(two ? 2 * T : 4 * T);
 #define W8A8_DOWN(JB, RB)                                                                                          \
-    lora_down_kernel<JB, RB, TR><<<grid, 64 * kDownWaves, 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, \
+    lora_down_kernel<JB, RB, TR><<<grid, 64 * down_waves(JB, RB), 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, \
                                                                        ranks, plan, v)
     switch (rank_blocks(R)) {
     case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
@@ -478,7 +571,7 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
 // the chip, each with a tile for every wave.
 int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
     const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L * (R > 64 ? 2 : 1);
-    int64_t s = (1024 + one - 1) / one;
+    int64_t s = (512 + one - 1) / one;
     if (s > (T + kOuterWaves - 1) / kOuterWaves) s = (T + kOuterWaves - 1) / kOuterWaves;
     return s < 1 ? 1 : s;
 }
