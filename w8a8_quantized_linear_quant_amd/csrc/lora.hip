@@ -27,13 +27,13 @@ struct Tile {
     int rows, adapter;
 };
 
-// Tile t of the plan; rows = 0 where the entry does not fit M and L.
+// Tile t of the plan; rows = 0 where the entry does not fit M and L (checked
+// without branches, so that the entry is one 16-byte scalar load).
 __device__ __forceinline__ Tile load_tile(const int32_t *plan, int t, int64_t M, int L) {
-    const int4 e = reinterpret_cast<const int4 *>(plan)[t];
-    Tile r = {e.x, e.y, e.z};
-    if (r.row0 < 0 || r.rows < 0 || r.rows > kTileRows || r.row0 + r.rows > M || r.adapter < -1 || r.adapter >= L)
-        r = {0, 0, -1};
-    return r;
+    const v4i e = reinterpret_cast<const v4i *>(plan)[t];
+    const int row0 = e[0], rows = e[1], adapter = e[2];
+    const bool ok = (row0 >= 0) & (rows >= 0) & (rows <= kTileRows) & (row0 <= M - rows) & (adapter >= -1) & (adapter < L);
+    return {ok ? row0 : 0, ok ? rows : 0, ok ? adapter : -1};
 }
 
 __device__ __forceinline__ int rank_of(const int32_t *ranks, int l, int R) {
@@ -373,12 +373,13 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
 }
 
 // --------------------------------------------------------------- outer sums
-// d[c][j] = sum over an adapter's rows of y[m][c] v[m][j], 128 columns c a
-// workgroup: its 4 waves take tiles in turn, each with sums of its own that
-// meet in LDS.  The contraction runs over rows, across memory: a lane loads 8
-// rows of 8 columns and pairs their halves into the 8 fragments (MFMA t has
-// column 8 i + t as its row i).  v is three bf16 parts, which hold all 24 bits
-// of it, so the gradients are as exact as f32 sums are.
+// d[c][j] = sum over an adapter's rows of y[m][c] v[m][j]: a product whose
+// contraction runs over rows, across memory in both factors.  A workgroup
+// takes 128 columns c and all ranks j; a tile of 64 rows of y and of v is
+// staged in LDS as it lies, and the fragments come back transposed
+// (ds_read_b64_tr_b16).  Two tiles' loads are in flight in registers.  v is
+// three bf16 parts, which hold all 24 bits of it, so the gradients are as
+// exact as f32 sums are.
 constexpr int kOuterWaves = 4;
 
 struct Outer {
@@ -387,124 +388,162 @@ struct Outer {
     const float *v;   // f32 [M, R]
     float *d;         // split s of d starts at s * L * R * C
     int C, groups;    // columns; workgroups of 128 columns
-    bool ranks_first; // [R, C] or [C, R]
 };
 struct OuterPair {
-    Outer a, b;       // dA: y = x, v = g; dB: y = dy, v = u
+    Outer a, b;       // dA [R, C]: y = x, v = g; dB [C, R]: y = dy, v = u
 };
 
-// Eight f32 values as three bf16 parts: the first two are cut (not rounded)
-// off the remainder, so each remainder is exact; an infinity or NaN has none.
-__device__ __forceinline__ void split3(const float *f, v4u (&s)[3]) {
+// Four f32 values as three bf16 parts: the first two are cut (not rounded) off
+// the remainder, so each remainder is exact; an infinity or NaN has none.
+__device__ __forceinline__ void split3(v4f f, uint2 (&s)[3]) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        float a = f[2 * p], b = f[2 * p + 1];
+    for (int i = 0; i < 2; ++i) {
+        uint32_t h[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float ha = __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), hb = __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
-            s[i][p] = halves(__float_as_uint(a), __float_as_uint(b), true);
-            a = i || __builtin_isfinite(a) ? a - ha : 0.f;
-            b = i || __builtin_isfinite(b) ? b - hb : 0.f;
-        }
-        s[2][p] = pack_bf16x2(a, b);
+        for (int p = 0; p < 2; ++p) h[p] = halves(__float_as_uint(f[2 * p]), __float_as_uint(f[2 * p + 1]), true);
+        s[i] = make_uint2(h[0], h[1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            f[k] = i || __builtin_isfinite(f[k]) ? f[k] - __uint_as_float(__float_as_uint(f[k]) & 0xFFFF0000u) : 0.f;
     }
+    s[2] = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+
+// Rows of PIECES 32-byte pieces in LDS (16 columns each): piece p of row m in
+// place p ^ turn(m), so that the 16 rows of a transposed read spread evenly
+// over the banks.
+template <int PIECES>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    const int turn = PIECES >= 4 ? row & 3 : PIECES == 2 ? row >> 1 & 1 : 0;
+    return row * (32 * PIECES) + ((piece ^ turn) << 5);
+}
+// Fragment of 16 columns (lane % 16) by rows 8 (lane / 16) .. + 7 of 32 from row m0.
+template <int PIECES>
+__device__ __forceinline__ v4u read_transposed(const char *area, int m0, int piece, int lane) {
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const int row = m0 + 8 * (lane >> 4) + (lane & 15) / 4, at = (lane & 3) * 8;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(area + piece_at<PIECES>(row, piece) + at));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(area + piece_at<PIECES>(row + 4, piece) + at));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return v4u{a.x, a.y, b.x, b.y};
+}
+
+// Block q of dA's or dB's: by adapter, split, columns.
+template <int JB, bool RANKS_FIRST>
+__device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, int L, int R, const int32_t *ranks,
+                                            const int32_t *plan, int T, int splits, char *ys,
+                                            char (&vs)[3][kTileRows * 32 * JB]) {
+    constexpr int kThreads = 64 * kOuterWaves;
+    // a wave's part of the 128 x 16 JB output: NC x NJ blocks of 16 x 16
+    constexpr int NC = JB == 1 ? 2 : 4, NJ = JB == 1 ? 1 : JB / 2;
+    const int col0 = q % o.groups * 128;
+    q /= o.groups;
+    const int split = q % splits, l = q / splits;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int pc = JB == 1 ? wave * 2 : (wave & 1) * 4, pj = JB == 1 ? 0 : (wave >> 1) * NJ;  // its first pieces
+    const int r = rank_of(ranks, l, R);
+    const int32_t *first = plan + 4 * (int64_t)T;
+    const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
+    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits);
+    const int end = r > 0 ? t0 + (int)((int64_t)n * (split + 1) / splits) : begin;
+    v4f acc[NC][NJ];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[c][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    // lane i of every wave holds the entry of tile i of the 64 under way, so
+    // that no scalar load (which would drain the LDS counter) is in the loop
+    for (int c0 = begin; c0 < end; c0 += 64) {
+        const int count = min(end - c0, 64);
+        Tile mine = load_tile(plan, c0 + min(lane, count - 1), M, L);
+        if (lane >= count) mine.rows = 0;
+        const int entry_row = (int)mine.row0, entry_rows = mine.rows;
+        v4u yd[2][4], vd[2][JB];
+        // Past the last tile a fetch reads 0, without a branch, so that each
+        // tile's loads are waited for by themselves.
+        auto fetch = [&](int i, v4u (&y)[4], v4u (&v)[JB]) {
+            const int row0 = __builtin_amdgcn_readlane(entry_row, min(i, 63));
+            const int rows = i < count ? __builtin_amdgcn_readlane(entry_rows, min(i, 63)) : 0;
+            // rows past the tile read 0 in both; columns past C are not stored
+            const auto ry = rows_rsrc(o.y, row0, rows, o.ldy, o.C);
+            const auto rv = v_rsrc(o.v, row0, rows, R);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[k] = load16(ry, (int)((k * 16 + (int)(threadIdx.x >> 4)) * o.ldy + col0 + 8 * (int)(threadIdx.x & 15)) * 2);
+#pragma unroll
+            for (int k = 0; k < JB; ++k) {
+                const int q = k * kThreads + threadIdx.x, row = q / (4 * JB), j = q % (4 * JB) * 4;
+                v[k] = load16(rv, j < R ? (row * R + j) * 4 : kOobOffset);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        fetch(0, yd[0], vd[0]);
+        fetch(1, yd[1], vd[1]);
+        for (int i = 0; i < count; i += 2) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                // (an odd count's last turn adds the 0 of a tile past the end)
+                __syncthreads();  // the last tile's fragments have been read
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = k * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+                    *reinterpret_cast<v4u *>(ys + piece_at<8>(row, c >> 1) + (c & 1) * 16) = yd[p][k];
+                }
+#pragma unroll
+                for (int k = 0; k < JB; ++k) {
+                    const int q = k * kThreads + threadIdx.x, row = q / (4 * JB), j = q % (4 * JB) * 4;
+                    uint2 s[3];
+                    split3(__builtin_bit_cast(v4f, vd[p][k]), s);
+#pragma unroll
+                    for (int h = 0; h < 3; ++h)
+                        *reinterpret_cast<uint2 *>(vs[h] + piece_at<JB>(row, j >> 4) + (j & 15) * 2) = s[h];
+                }
+                fetch(i + p + 2, yd[p], vd[p]);
+                __syncthreads();
+#pragma unroll
+                for (int m0 = 0; m0 < kTileRows; m0 += 32) {
+                    v4u yf[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) yf[c] = read_transposed<8>(ys, m0, pc + c, lane);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int h = 0; h < 3; ++h) {
+                            const v4u f = read_transposed<JB>(vs[h], m0, pj + j, lane);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c)
+                                acc[c][j] = RANKS_FIRST ? mfma(f, yf[c], acc[c][j]) : mfma(yf[c], f, acc[c][j]);
+                        }
+                }
+            }
+        }
+    }
+    // the contiguous index of d along 16 lanes: rows of the product are ranks
+    // (dA) or columns (dB)
+    float *d = o.d + ((int64_t)split * L + l) * R * o.C;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int b = 0; b < NJ; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int across = 4 * (lane >> 4) + e, along = lane & 15;
+                const int col = col0 + (pc + c) * 16 + (RANKS_FIRST ? along : across);
+                const int j = (pj + b) * 16 + (RANKS_FIRST ? across : along);
+                if (col < o.C && j < R) d[RANKS_FIRST ? (int64_t)j * o.C + col : (int64_t)col * R + j] = j < r ? acc[c][b][e] : 0.f;
+            }
 }
 
 template <int JB>
 __global__ __launch_bounds__(64 * kOuterWaves) void lora_outer_kernel(OuterPair both, int64_t M, int L, int R,
                                                                       const int32_t *ranks, const int32_t *plan, int T,
-                                                                      int splits, int j_parts) {
-    __shared__ float sums[kOuterWaves][8][64];
-    // blocks: dA's, then dB's; of each by adapter, split, part of the rank, columns
-    const int per = L * splits * j_parts;
-    const bool is_a = (int)blockIdx.x < both.a.groups * per;
-    const Outer &o = is_a ? both.a : both.b;
-    int q = is_a ? blockIdx.x : blockIdx.x - both.a.groups * per;
-    const int col0 = q % o.groups * 128;
-    q /= o.groups;
-    const int j0 = q % j_parts * (16 * JB);
-    q /= j_parts;
-    const int split = q % splits, l = q / splits;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fi = lane & 15, fg = lane >> 4;
-    const int r = rank_of(ranks, l, R);
-    const int32_t *first = plan + 4 * (int64_t)T;
-    const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
-    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits), end = t0 + (int)((int64_t)n * (split + 1) / splits);
-    v4f acc[8][JB];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int b = 0; b < JB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
-
-    if (j0 < r && begin + wave < end) {
-        // 32 rows a step, the next step's loads in flight while one is worked on
-        int i = begin + wave, m0 = 0;
-        Tile tile = load_tile(plan, i, M, L), next = tile;
-        if (i + kOuterWaves < end) next = load_tile(plan, i + kOuterWaves, M, L);
-        v4u d[8];
-        float f[JB][8];
-        auto fetch = [&]() {
-            // rows past the tile read 0 in both; columns past C are not stored
-            const auto ry = rows_rsrc(o.y, tile.row0, tile.rows, o.ldy, o.C);
-            const auto rv = v_rsrc(o.v, tile.row0, tile.rows, R);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = load16(ry, (int)((m0 + 8 * fg + k) * o.ldy + col0 + 8 * fi) * 2);
-#pragma unroll
-            for (int b = 0; b < JB; ++b)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    f[b][k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                        rv, ((m0 + 8 * fg + k) * R + j0 + b * 16 + fi) * 4, 0, 0));
-        };
-        fetch();
-        while (true) {
-            v4u yf[8];
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) yf[t][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
-            v4u s[JB][3];
-#pragma unroll
-            for (int b = 0; b < JB; ++b) split3(f[b], s[b]);
-            m0 += 32;
-            if (m0 >= tile.rows) {
-                i += kOuterWaves, m0 = 0;
-                tile = next;
-                if (i + kOuterWaves < end) next = load_tile(plan, i + kOuterWaves, M, L);
-            }
-            const bool more = i < end;
-            if (more) fetch();
-#pragma unroll
-            for (int b = 0; b < JB; ++b)
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t][b] = mfma(yf[t], s[b][k], acc[t][b]);
-            if (!more) break;
-        }
-    }
-    // lane's (t, b, e): column 8 (4 fg + e) + t, rank 16 b + fi
-    float *d = o.d + ((int64_t)split * L + l) * R * o.C;
-#pragma unroll
-    for (int b = 0; b < JB; ++b) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            __syncthreads();
-#pragma unroll
-            for (int t = 0; t < 8; ++t) sums[wave][t][lane] = acc[t][b][e];
-            __syncthreads();
-            for (int i = threadIdx.x; i < 512; i += 64 * kOuterWaves) {
-                // consecutive threads along the contiguous index of d
-                const int t = o.ranks_first ? i & 7 : i >> 6, g = o.ranks_first ? i >> 3 & 3 : i >> 4 & 3;
-                const int jj = o.ranks_first ? i >> 5 : i & 15;
-                float s = 0.f;
-#pragma unroll
-                for (int k = 0; k < kOuterWaves; ++k) s += sums[k][t][g * 16 + jj];
-                const int c = col0 + 8 * (4 * g + e) + t, j = j0 + b * 16 + jj;
-                if (c < o.C && j < R) d[o.ranks_first ? (int64_t)j * o.C + c : (int64_t)c * R + j] = j < r ? s : 0.f;
-            }
-        }
-    }
+                                                                      int splits) {
+    __shared__ __attribute__((aligned(16))) char ys[kTileRows * 256], vs[3][kTileRows * 32 * JB];
+    const int na = both.a.groups * L * splits, q = blockIdx.x;
+    if (q < na) outer_block<JB, true>(both.a, q, M, L, R, ranks, plan, T, splits, ys, vs);
+    else outer_block<JB, false>(both.b, q - na, M, L, R, ranks, plan, T, splits, ys, vs);
 }
 
 // da = sum of its splits [splits][na], db likewise (na, nb multiples of 4).
@@ -567,13 +606,12 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
 #undef W8A8_UP
 }
 
-// Over how many workgroups an adapter's rows are split: enough of them for
-// the chip, each with a tile for every wave.
-int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
-    const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L * (R > 64 ? 2 : 1);
-    int64_t s = (512 + one - 1) / one;
-    if (s > (T + kOuterWaves - 1) / kOuterWaves) s = (T + kOuterWaves - 1) / kOuterWaves;
-    return s < 1 ? 1 : s;
+// Over how many workgroups an adapter's rows are split: two for each CU, each
+// with two tiles or more of an adapter with its share of the rows.
+int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t L) {
+    const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L, most = T / (2 * L);
+    const int64_t s = (512 + one - 1) / one;
+    return s < most ? s : most < 1 ? 1 : most;
 }
 
 constexpr int64_t kMaxWidth = 1 << 22;
@@ -667,7 +705,7 @@ extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int
 extern "C" size_t lora_backward_workspace_bytes(int64_t M, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
     using namespace w8a8;
     if (M < 0 || T < 0 || K < 8 || N < 8 || L < 1 || R < 8 || R > kMaxR) return 0;
-    const int64_t splits = outer_splits(T, K, N, R, L);
+    const int64_t splits = outer_splits(T, K, N, L);
     return (size_t)(M * R + (splits > 1 ? splits * L * R * (K + N) : 0)) * sizeof(float);
 }
 
@@ -694,20 +732,20 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         if (dx) up_launch<true>(g, a, M, K, L, R, ranks, plan, T, base, ldbase, dx, lddx, stream);
     }
     if (da) {
-        const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
-        const int j_parts = R > 64 ? 2 : 1;
+        const int64_t splits = outer_splits(T, K, N, L), na = L * R * K, nb = L * R * N;
         const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
-        const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga, true},
-                                {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb, false}};
-        const int64_t grid = (ga + gb) * L * splits * j_parts;
+        const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga},
+                                {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb}};
+        const int64_t grid = (ga + gb) * L * splits;
         if (grid > INT32_MAX) return W8A8_ERR_SHAPE;
 #define W8A8_OUTER(JB)                                                                                        \
     lora_outer_kernel<JB><<<(int)grid, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan,   \
-                                                                     (int)T, (int)splits, j_parts)
+                                                                     (int)T, (int)splits)
         switch (rank_blocks(R)) {
         case 1: W8A8_OUTER(1); break;
         case 2: W8A8_OUTER(2); break;
-        default: W8A8_OUTER(4); break;
+        case 4: W8A8_OUTER(4); break;
+        default: W8A8_OUTER(8); break;
         }
 #undef W8A8_OUTER
         if (splits > 1)
