@@ -107,18 +107,97 @@ __device__ __forceinline__ v4u transposed_fragment(const char *area, int jb, int
     return v4u{a.x, a.y, b.x, b.y};
 }
 
+// acc += this wave's slices of rows x weight, for the 16 RB rows from `first`
+// of a tile; area: the wave's LDS; block: which workgroup asks (all that share
+// a result must give the same, for the order of its sums).
+template <int JB, int RB, bool TR, int W>
+__device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x, const Tile &tile, int first, int C,
+                                          int64_t ldx, const uint16_t *w, int R, char *area, unsigned block) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int slices = (C + kSlice - 1) / kSlice;
+    if (wave >= slices) return;
+    const auto rx = rows_rsrc(x, tile.row0 + first, tile.rows - first, ldx, C);
+    const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)tile.adapter * R * C, (short)0,
+                                                      R * C * 2, kBufferRsrcWord3);
+            const int li = lane >> 4, lc = (lane & 15) * 8;  // row and column of a lane in a load of 4 rows x 128
+    // past C both factors read 0: neither may be whatever lies behind a row
+    auto fetch_x = [&](int slice, int a, v4u (&d)[4]) {
+        const int k = slice * kSlice + lc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = load16(rx, k < C ? (int)((a * 16 + i * 4 + li) * ldx + k) * 2 : kOobOffset);
+    };
+    constexpr int kUnits = TR ? 4 : JB, kUnit = TR ? JB : 4;  // weight blocks of a slice, loads of a block
+    auto fetch_w = [&](int slice, int unit, v4u (&d)[kUnit]) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            if constexpr (TR) {  // 32 rows n of a step, all ranks
+                const int c = i * 64 + lane, row = slice * kSlice + unit * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
+                d[i] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
+            } else {             // 16 ranks of a slice
+                const int k = slice * kSlice + lc;
+                d[i] = load16(rw, k < C ? ((unit * 16 + i * 4 + li) * C + k) * 2 : kOobOffset);
+            }
+        }
+    };
+    // Workgroups start at different slices: in step, they would all read
+    // the same few kilobytes of every row (with rows a power of two apart
+    // a quarter of the memory channels) and the same lines of the weight
+    // (8 XCDs: blocks 8 apart share an L2).
+    const int turns = (slices + W - 1) / W;
+    int turn = (int)((block / 8 + block) % (unsigned)turns);
+    v4u xd[RB][4], wd[kUnit];
+    int slice = turn * W + wave;
+#pragma unroll
+    for (int a = 0; a < RB; ++a) fetch_x(slice, a, xd[a]);
+    fetch_w(slice, 0, wd);
+    for (int n = 0; n < turns; ++n) {  // a slice past the end reads 0 without touching memory
+        turn = turn + 1 < turns ? turn + 1 : 0;
+        const int next = n + 1 < turns ? turn * W + wave : slices;
+        v4u xf[RB][4];
+#pragma unroll
+        for (int a = 0; a < RB; ++a) {
+            turn_in(area, xd[a], lane);
+            fetch_x(next, a, xd[a]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) xf[a][t] = turn_out(area, t, lane);
+        }
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) {
+            if constexpr (TR) {
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 16) = wd[i];
+            } else {
+                turn_in(area, wd, lane);
+            }
+            if (q + 1 < kUnits) fetch_w(slice, q + 1, wd);
+            else fetch_w(next, 0, wd);
+#pragma unroll
+            for (int i = 0; i < (TR ? JB : 4); ++i) {
+                const v4u f = TR ? transposed_fragment<JB>(area, i, lane) : turn_out(area, i, lane);
+                const int t = TR ? q : i, b = TR ? i : q;
+#pragma unroll
+                for (int a = 0; a < RB; ++a) acc[a][b] = mfma(xf[a][t], f, acc[a][b]);
+            }
+        }
+        slice = next;
+    }
+}
+
 template <int JB, int RB, bool TR>
-__global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
-                                                                    const uint16_t *w, int L, int R,
-                                                                    const float *scale, const int32_t *ranks,
-                                                                    const int32_t *plan, float *v) {
+__global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(const uint16_t *x, int64_t M, int C,
+                                                                            int64_t ldx, const uint16_t *w, int L,
+                                                                            int R, const float *scale,
+                                                                            const int32_t *ranks, const int32_t *plan,
+                                                                            int T, float *v) {
     constexpr int W = down_waves(JB, RB);
     constexpr int kArea = TR && JB > 4 ? JB * 1024 : 4096;  // bytes of a wave
     constexpr int kSums = W * RB * 16 * 17 * 4;
     __shared__ __attribute__((aligned(16))) char lds[W * kArea > kSums ? W * kArea : kSums];
-    constexpr int kParts = 4 / RB;
-    const Tile tile = load_tile(plan, blockIdx.x / kParts, M, L);
-    const int first = (blockIdx.x % kParts) * (16 * RB);
+    // the tiles' first parts come first: short tiles have no others, and the
+    // blocks that are left must not fall on the same few XCDs
+    const Tile tile = load_tile(plan, blockIdx.x % T, M, L);
+    const int first = blockIdx.x / T * (16 * RB);
     if (first >= tile.rows) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = rank_of(ranks, tile.adapter, R);
@@ -128,77 +207,7 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
     for (int a = 0; a < RB; ++a)
 #pragma unroll
         for (int b = 0; b < JB; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
-
-    const int slices = (C + kSlice - 1) / kSlice;
-    if (r > 0 && wave < slices) {  // r: the same for the whole workgroup
-        const auto rx = rows_rsrc(x, tile.row0 + first, tile.rows - first, ldx, C);
-        const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)tile.adapter * R * C, (short)0,
-                                                          R * C * 2, kBufferRsrcWord3);
-        char *area = lds + wave * kArea;
-        const int li = lane >> 4, lc = (lane & 15) * 8;  // row and column of a lane in a load of 4 rows x 128
-        // past C both factors read 0: neither may be whatever lies behind a row
-        auto fetch_x = [&](int slice, int a, v4u (&d)[4]) {
-            const int k = slice * kSlice + lc;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                d[i] = load16(rx, k < C ? (int)((a * 16 + i * 4 + li) * ldx + k) * 2 : kOobOffset);
-        };
-        constexpr int kUnits = TR ? 4 : JB, kUnit = TR ? JB : 4;  // weight blocks of a slice, loads of a block
-        auto fetch_w = [&](int slice, int unit, v4u (&d)[kUnit]) {
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) {
-                if constexpr (TR) {  // 32 rows n of a step, all ranks
-                    const int c = i * 64 + lane, row = slice * kSlice + unit * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
-                    d[i] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
-                } else {             // 16 ranks of a slice
-                    const int k = slice * kSlice + lc;
-                    d[i] = load16(rw, k < C ? ((unit * 16 + i * 4 + li) * C + k) * 2 : kOobOffset);
-                }
-            }
-        };
-        // Workgroups start at different slices: in step, they would all read
-        // the same few kilobytes of every row (with rows a power of two apart
-        // a quarter of the memory channels) and the same lines of the weight
-        // (8 XCDs: blocks 8 apart share an L2).
-        const int turns = (slices + W - 1) / W;
-        int turn = (int)((blockIdx.x / 8 + blockIdx.x) % (unsigned)turns);
-        v4u xd[RB][4], wd[kUnit];
-        int slice = turn * W + wave;
-#pragma unroll
-        for (int a = 0; a < RB; ++a) fetch_x(slice, a, xd[a]);
-        fetch_w(slice, 0, wd);
-        for (int n = 0; n < turns; ++n) {  // a slice past the end reads 0 without touching memory
-            turn = turn + 1 < turns ? turn + 1 : 0;
-            const int next = n + 1 < turns ? turn * W + wave : slices;
-            v4u xf[RB][4];
-#pragma unroll
-            for (int a = 0; a < RB; ++a) {
-                turn_in(area, xd[a], lane);
-                fetch_x(next, a, xd[a]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) xf[a][t] = turn_out(area, t, lane);
-            }
-#pragma unroll
-            for (int q = 0; q < kUnits; ++q) {
-                if constexpr (TR) {
-#pragma unroll
-                    for (int i = 0; i < kUnit; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 16) = wd[i];
-                } else {
-                    turn_in(area, wd, lane);
-                }
-                if (q + 1 < kUnits) fetch_w(slice, q + 1, wd);
-                else fetch_w(next, 0, wd);
-#pragma unroll
-                for (int i = 0; i < (TR ? JB : 4); ++i) {
-                    const v4u f = TR ? transposed_fragment<JB>(area, i, lane) : turn_out(area, i, lane);
-                    const int t = TR ? q : i, b = TR ? i : q;
-#pragma unroll
-                    for (int a = 0; a < RB; ++a) acc[a][b] = mfma(xf[a][t], f, acc[a][b]);
-                }
-            }
-            slice = next;
-        }
-    }
+    if (r > 0) down_sums<JB, RB, TR, W>(acc, x, tile, first, C, ldx, w, R, lds + wave * kArea, blockIdx.x);
     auto part = reinterpret_cast<float (*)[RB * 16][17]>(lds);
 #pragma unroll
     for (int b = 0; b < JB; ++b) {
@@ -246,6 +255,106 @@ __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, bool high) {
     return __builtin_amdgcn_perm(b, a, high ? 0x07060302u : 0x05040100u);
 }
 
+// The weight fragments of a wave's 128 columns, one 32-wide contraction k at a
+// time: loaded with lanes along memory, then turned into wf[t][k].  Entries
+// beyond the adapter's rank become 0, whatever lies there.  TR: 8 ranks of the
+// lane's 8 columns, paired into the 8 fragments.  Else: 128 rows of 2 or 4
+// chunks of 8 ranks through the wave's own LDS (4 KB for JB = 1, else 8),
+// slots swizzled for the reads 8 rows apart.
+constexpr int up_loads(int JB, bool TR) { return JB == 1 && !TR ? 4 : 8; }
+
+template <bool TR>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t up_rsrc(const uint16_t *w, int adapter, int C, int R, int r) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)adapter * R * C, (short)0,
+                                             (TR ? r : R) * C * 2, kBufferRsrcWord3);
+}
+
+template <int JB, bool TR>
+__device__ __forceinline__ void up_fetch(v4u (&d)[up_loads(JB, TR)], __amdgpu_buffer_rsrc_t rw, int col0, int C, int R,
+                                         int k) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < up_loads(JB, TR); ++i) {
+        if constexpr (TR) {
+            const int jg = JB == 1 ? lane >> 4 & 1 : lane >> 4, j = k * 32 + jg * 8 + i, c = col0 + 8 * (lane & 15);
+            d[i] = load16(rw, c < C ? (j * C + c) * 2 : kOobOffset);
+        } else {
+            constexpr int kCh = JB == 1 ? 2 : 4;
+            const int q = i * 64 + lane, n = col0 + q / kCh, j = k * 32 + q % kCh * 8;
+            d[i] = load16(rw, n < C && j < R ? (n * R + j) * 2 : kOobOffset);
+        }
+    }
+}
+
+template <int JB, bool TR, int KB>
+__device__ __forceinline__ void up_fragments(v4u (&wf)[8][KB], int k, const v4u (&d)[up_loads(JB, TR)], char *ws, int R,
+                                             int r) {
+    const int lane = threadIdx.x & 63, fi = lane & 15, jg = JB == 1 ? lane >> 4 & 1 : lane >> 4;
+    if constexpr (TR) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) wf[t][k][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
+    } else {
+        constexpr int kCh = JB == 1 ? 2 : 4;
+#pragma unroll
+        for (int i = 0; i < 2 * kCh; ++i) {
+            const int q = i * 64 + lane;
+            *reinterpret_cast<v4u *>(ws + ((q ^ (q / kCh >> 3 & 7)) << 4)) = d[i];
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int q = (8 * fi + t) * kCh + jg;
+            wf[t][k] = *reinterpret_cast<const v4u *>(ws + ((q ^ (fi & 7)) << 4));
+        }
+        if (r < R) {
+            const int j = k * 32 + jg * 8;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t keep = (j + 2 * p < r ? 0xFFFFu : 0u) | (j + 2 * p + 1 < r ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) wf[t][k][p] &= keep;
+            }
+        }
+    }
+}
+
+// One block of 16 rows of a wave's 128 columns: base (bf) plus v (its halves in
+// LDS rows hi, lo of this block) times the weight, stored.
+template <int JB, int KB, int P>
+__device__ __forceinline__ void up_rows(const v4u (&bf)[4], const uint16_t (*hi)[P], const uint16_t (*lo)[P],
+                                        const v4u (&wf)[8][KB], int r, uint16_t *out, int64_t ldout, int rows, int col0,
+                                        int C) {
+    const int lane = threadIdx.x & 63, fi = lane & 15, fg = lane >> 4, jg = JB == 1 ? fg & 1 : fg;
+    v4f acc[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = __uint_as_float(t & 1 ? bf[e][t / 2] & 0xFFFF0000u : bf[e][t / 2] << 16);
+    if (r > 0) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+            for (int h = 0; h < (JB == 1 ? 1 : 2); ++h) {
+                const uint16_t(*v)[P] = (JB == 1 ? fg >> 1 : h) ? lo : hi;
+                const v4u f = *reinterpret_cast<const v4u *>(&v[fi][k * 32 + jg * 8]);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) acc[t] = mfma(f, wf[t][k], acc[t]);
+            }
+        }
+    }
+    const int c = col0 + 8 * fi;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int row = 4 * fg + e;
+        if (row >= rows || c >= C) continue;
+        v4u d;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
+        *reinterpret_cast<v4u *>(out + row * ldout + c) = d;
+    }
+}
+
 template <int JB, bool TR>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
                                                                 int L, int R, const int32_t *ranks,
@@ -270,7 +379,6 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
     }
     const int r = rank_of(ranks, tile.adapter, R);
     const int fi = lane & 15, fg = lane >> 4;
-    const int jg = JB == 1 ? fg & 1 : fg;  // this lane's 8 ranks of a contraction
 
     v4u bf[RB][4];
     const auto rb = rows_rsrc(base, tile.row0, base ? tile.rows : 0, ldbase, C);
@@ -280,53 +388,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) bf[a][e] = load16(rb, (int)((a * 16 + 4 * fg + e) * ldbase + col0 + 8 * fi) * 2);
     }
-    // weight fragments: entries beyond the adapter's rank are 0, whatever lies there
     v4u wf[8][KB];
     if (r > 0 && col0 < C) {
-        const uint16_t *wl = w + (int64_t)tile.adapter * R * C;
-        const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(wl), (short)0, (TR ? r : R) * C * 2, kBufferRsrcWord3);
+        const auto rw = up_rsrc<TR>(w, tile.adapter, C, R, r);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-            const int j = k * 32 + jg * 8;
-            if constexpr (TR) {
-                // 8 ranks of the lane's 8 columns, paired into the 8 fragments
-                const int c = col0 + 8 * fi;
-                v4u d[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = load16(rw, c < C ? ((j + i) * C + c) * 2 : kOobOffset);
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) wf[t][k][p] = halves(d[2 * p][t / 2], d[2 * p + 1][t / 2], t & 1);
-            } else {
-                // 128 rows of the contraction's kCh chunks of 8 ranks through the
-                // wave's own LDS, slots swizzled for the reads 8 rows apart
-                constexpr int kCh = JB == 1 ? 2 : 4;
-                v4u d[2 * kCh];
-#pragma unroll
-                for (int i = 0; i < 2 * kCh; ++i) {
-                    const int q = i * 64 + lane, n = q / kCh, jc = k * 32 + q % kCh * 8;
-                    d[i] = load16(rw, col0 + n < C && jc < R ? ((col0 + n) * R + jc) * 2 : kOobOffset);
-                }
-#pragma unroll
-                for (int i = 0; i < 2 * kCh; ++i) {
-                    const int q = i * 64 + lane, n = q / kCh;
-                    *reinterpret_cast<v4u *>(ws[wave] + ((q ^ (n >> 3 & 7)) << 4)) = d[i];
-                }
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const int q = (8 * fi + t) * kCh + jg;
-                    wf[t][k] = *reinterpret_cast<const v4u *>(ws[wave] + ((q ^ (fi & 7)) << 4));
-                }
-                if (r < R) {
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const uint32_t keep = (j + 2 * p < r ? 0xFFFFu : 0u) | (j + 2 * p + 1 < r ? 0xFFFF0000u : 0u);
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) wf[t][k][p] &= keep;
-                    }
-                }
-            }
+            v4u d[up_loads(JB, TR)];
+            up_fetch<JB, TR>(d, rw, col0, C, R, k);
+            up_fragments<JB, TR>(wf, k, d, ws[TR ? 0 : wave], R, r);
         }
     }
 #pragma unroll
@@ -342,34 +411,68 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
 #pragma unroll
     for (int a = 0; a < RB; ++a) {
         if (a * 16 >= tile.rows) break;
-        v4f acc[8];
+        up_rows<JB, KB, P>(bf[a], &vs[0][a * 16], &vs[1][a * 16], wf, r, out + (tile.row0 + a * 16) * ldout, ldout,
+                           tile.rows - a * 16, col0, C);
+    }
+}
+
+// ---------------------------------------------------------------- both
+// The down- and the up-projection of 16 rows in one workgroup of 16 waves, 128
+// columns a wave: one launch, with base and the up-projection's weights loaded
+// ahead of the sums, ranks up to 16.  Where 2048 columns a workgroup do not cover C2, each
+// further one takes the sums again (`groups` workgroups a block of rows).
+template <bool TR>
+__global__ __launch_bounds__(1024) void lora_both_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
+                                                         const uint16_t *w, int L, int R, const float *scale,
+                                                         const int32_t *ranks, const int32_t *plan, int T, float *v,
+                                                         const uint16_t *w2, int C2, int groups, const uint16_t *base,
+                                                         int64_t ldbase, uint16_t *out, int64_t ldout) {
+    constexpr int W = 16, JB = 1, KB = 1, P = JB * 16 + 8, kArea = 4096;
+    __shared__ __attribute__((aligned(16))) char lds[W * kArea];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[2][16][P];
+    const unsigned block = blockIdx.x / groups;
+    const Tile tile = load_tile(plan, block % T, M, L);
+    const int first = block / T * 16;
+    if (first >= tile.rows) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = rank_of(ranks, tile.adapter, R);
+    const float s = tile.adapter >= 0 && scale ? scale[tile.adapter] : 1.f;
+    const int group = blockIdx.x % groups, col0 = (group * W + wave) * 128;
+    const int64_t row0 = tile.row0 + first;
+    const int rows = min(tile.rows - first, 16);
+    v4u bf[4], d[up_loads(JB, TR)], wf[8][KB];
+    const auto rb = rows_rsrc(base, row0, base ? rows : 0, ldbase, C2);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+    for (int e = 0; e < 4; ++e)
+        bf[e] = load16(rb, col0 < C2 ? (int)((4 * (lane >> 4) + e) * ldbase + col0 + 8 * (lane & 15)) * 2 : kOobOffset);
+    up_fetch<JB, TR>(d, up_rsrc<TR>(w2, max(tile.adapter, 0), C2, R, r), col0, C2, R, 0);
+    v4f acc[1][JB];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[t][e] = __uint_as_float(t & 1 ? bf[a][e][t / 2] & 0xFFFF0000u : bf[a][e][t / 2] << 16);
-        if (r > 0) {
+    for (int b = 0; b < JB; ++b) acc[0][b] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (r > 0) down_sums<JB, 1, TR, W>(acc, x, tile, first, C, ldx, w, R, lds + wave * kArea, block);
+    auto part = reinterpret_cast<float (*)[16][17]>(lds);
 #pragma unroll
-            for (int k = 0; k < KB; ++k) {
+    for (int b = 0; b < JB; ++b) {
+        __syncthreads();
 #pragma unroll
-                for (int h = 0; h < (JB == 1 ? 1 : 2); ++h) {
-                    const v4u f = *reinterpret_cast<const v4u *>(&vs[JB == 1 ? fg >> 1 : h][a * 16 + fi][k * 32 + jg * 8]);
+        for (int e = 0; e < 4; ++e) part[wave][4 * (lane >> 4) + e][lane & 15] = acc[0][b][e];
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int row = threadIdx.x / 16, j = b * 16 + threadIdx.x % 16;
+            float t = 0.f;
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = mfma(f, wf[t][k], acc[t]);
-                }
-            }
-        }
-        const int c = col0 + 8 * fi;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = a * 16 + 4 * fg + e;
-            if (row >= tile.rows || c >= C) continue;
-            v4u d;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
-            *reinterpret_cast<v4u *>(out + (tile.row0 + row) * ldout + c) = d;
+            for (int k = 0; k < W; ++k) t += part[k][row][threadIdx.x % 16];
+            t = j < r ? t * s : 0.f;
+            if (v && group == 0 && row < rows && j < R) v[(row0 + row) * R + j] = t;
+            const float hi = __uint_as_float(pack_bf16x2(t, 0.f) << 16);
+            vs[0][row][j] = (uint16_t)(__float_as_uint(hi) >> 16);
+            vs[1][row][j] = (uint16_t)pack_bf16x2(__builtin_isfinite(hi) ? t - hi : 0.f, 0.f);
         }
     }
+    __syncthreads();
+    if (col0 >= C2) return;
+    up_fragments<JB, TR>(wf, 0, d, lds + wave * kArea, R, r);
+    up_rows<JB, KB, P>(bf, vs[0], vs[1], wf, r, out + row0 * ldout, ldout, rows, col0, C2);
 }
 
 // --------------------------------------------------------------- outer sums
@@ -579,7 +682,7 @@ void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uin
     const int grid = (int)(two ? 2 * T : 4 * T);
 #define W8A8_DOWN(JB, RB)                                                                                          \
     lora_down_kernel<JB, RB, TR><<<grid, 64 * down_waves(JB, RB), 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, \
-                                                                       ranks, plan, v)
+                                                                       ranks, plan, (int)T, v)
     switch (rank_blocks(R)) {
     case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
     case 2: two ? W8A8_DOWN(2, 2) : W8A8_DOWN(2, 1); break;
@@ -606,12 +709,43 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
 #undef W8A8_UP
 }
 
-// Over how many workgroups an adapter's rows are split: two for each CU, each
-// with two tiles or more of an adapter with its share of the rows.
-int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t L) {
+// Whether the down- and the up-projection go in one launch: blocks of rows
+// times workgroups a block, and once more for the sums that each of a block's
+// workgroups repeats.  K = 4096, R = 16, one launch against two: 1 token and
+// 4096 columns 7.2 us against 7.8, 48 requests of one 7.6 against 8.6, 2039
+// tokens 13.8 against 15.0 (648); but 4096 tokens 34 against 21, 48 requests
+// and 12288 columns 16.7 against 10.5 (1836).  Ranks past 16 do not fit the
+// registers beside what is loaded ahead (32: 12.8 against 9.2 for 1 token).
+bool one_launch(int64_t M, int64_t T, int64_t C2, int64_t R) {
+    const int64_t groups = (C2 + 2047) / 2048;
+    return R <= 16 && (M / 16 + T) * groups * groups <= 650;
+}
+// out = base + (scale x w^T) w2^T; v [M, R] = scale x w^T is left where it is
+// not null (two launches need it).
+template <bool TR>
+void both_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uint16_t *w, int64_t L, int64_t R,
+                 const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T, float *v, const uint16_t *w2,
+                 int64_t C2, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout, hipStream_t stream) {
+    if (one_launch(M, T, C2, R)) {
+        const int groups = (int)((C2 + 2047) / 2048);
+        lora_both_kernel<TR><<<(int)(4 * T * groups), 1024, 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, ranks, plan, (int)T, v, w2,
+                                                           (int)C2, groups, base, ldbase, out, ldout);
+        return;
+    }
+    down_launch<TR>(x, M, C, ldx, w, L, R, scale, ranks, plan, T, v, stream);
+    up_launch<TR>(v, w2, M, C2, L, R, ranks, plan, T, base, ldbase, out, ldout, stream);
+}
+
+// Over how many workgroups an adapter's rows are split.  Each split's sums are
+// written and read again (with the launch that adds them up), so one workgroup
+// for each CU is enough; from R = 64 on a workgroup's products and LDS reads
+// take as long as its loads, and two for each CU overlap them.  Both
+// gradients, with the down-projection, M 8192, K = N 4096, 1, 4, 8, 16 splits:
+// R 32 112, 45, 45, 46 us; R 64 169, 63, 56, 64 us.
+int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
     const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L, most = T / (2 * L);
-    const int64_t s = (512 + one - 1) / one;
-    return s < most ? s : most < 1 ? 1 : most;
+    const int64_t s = (R <= 32 ? 256 : 512) / one;
+    return s < most ? (s < 1 ? 1 : s) : most < 1 ? 1 : most;
 }
 
 constexpr int64_t kMaxWidth = 1 << 22;
@@ -697,15 +831,14 @@ extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int
     if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(u) || !aligned16(workspace))
         return W8A8_ERR_ALIGN;
     float *v = u ? u : static_cast<float *>(workspace);
-    down_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, stream);
-    up_launch<false>(v, b, M, N, L, R, ranks, plan, T, base, ldbase, out, ldout, stream);
+    both_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, b, N, base, ldbase, out, ldout, stream);
     return launch_status();
 }
 
 extern "C" size_t lora_backward_workspace_bytes(int64_t M, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
     using namespace w8a8;
     if (M < 0 || T < 0 || K < 8 || N < 8 || L < 1 || R < 8 || R > kMaxR) return 0;
-    const int64_t splits = outer_splits(T, K, N, L);
+    const int64_t splits = outer_splits(T, K, N, R, L);
     return (size_t)(M * R + (splits > 1 ? splits * L * R * (K + N) : 0)) * sizeof(float);
 }
 
@@ -728,11 +861,11 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         return W8A8_ERR_ALIGN;
     float *g = static_cast<float *>(workspace), *parts = g + M * R;
     if (T > 0) {
-        down_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, stream);
-        if (dx) up_launch<true>(g, a, M, K, L, R, ranks, plan, T, base, ldbase, dx, lddx, stream);
+        if (dx) both_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, a, K, base, ldbase, dx, lddx, stream);
+        else down_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, stream);
     }
     if (da) {
-        const int64_t splits = outer_splits(T, K, N, L), na = L * R * K, nb = L * R * N;
+        const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
         const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
         const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga},
                                 {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb}};
