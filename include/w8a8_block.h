@@ -8,7 +8,9 @@
  * by the caller, arguments checked on the host before anything is launched,
  * kernels enqueued on `stream` without allocation, clearing or
  * synchronization (graph-capturable), sizes of 0 a successful no-op (but sums
- * over no rows are written as zero), base pointers 16-byte aligned.  Results do not depend on the order in which
+ * over no rows are written as zero), base pointers 16-byte aligned.  An output
+ * overlaps no other argument, except where a declaration says that it may be
+ * one of them.  Results do not depend on the order in which
  * workgroups run (no atomics): the same call gives the same bits.  Infinities
  * and NaN follow the formulas and stay in the rows, requests and columns
  * whose formulas hold them.

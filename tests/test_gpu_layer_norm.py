@@ -123,8 +123,10 @@ def test_without_weight_or_bias(w8, xt, weight, bias):
     _check(w8, 21, 777, xt, xt, weight, bias)
 
 
-@pytest.mark.parametrize("M,K", [(1500, 256), (4099, 72), (2600, 1032), (1030, 4104), (700, 8192)])
+@pytest.mark.parametrize("M,K", [(1500, 256), (9001, 72), (2600, 1032), (1030, 4104), (700, 8192),
+                                 (5000, 2200), (2500, 4201)])
 def test_many_rows(w8, M, K):
+    """Several rows a workgroup, forward and backward."""
     _check(w8, M, K, "bf16", "f32", seed=K)
 
 
@@ -229,7 +231,7 @@ def test_rows_past_32_bit_offsets(w8):
 # ----------------------------------------------------------------- to codes
 @pytest.mark.parametrize("qt", [0, 1])
 @pytest.mark.parametrize("xt,M,K", [("bf16", 1, 16), ("bf16", 5, 1280), ("f32", 7, 1001), ("bf16", 130, 4096), ("f32", 3, 8208),
-                                    ("bf16", 3, 17000), ("bf16", 2, 33)])
+                                    ("bf16", 3, 17000), ("bf16", 2, 33), ("bf16", 5000, 2208), ("f32", 8300, 50)])
 def test_codes(w8, qt, xt, M, K):
     """Scales are absmax / QMAX of the exact norm within its error; each code
     stands for a value within half a step (and y's error) of the exact one;

@@ -134,6 +134,20 @@ def test_against_the_definition(w8, case):
     _check(w8, Batch(lengths, adapters, K, N, R, L, seed=len(lengths) + K), str(case[2:]))
 
 
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 128])
+def test_many_rows(w8, R):
+    """Enough rows for 32 of them a workgroup, two launches at every rank and
+    an adapter's rows split over workgroups."""
+    _check(w8, Batch([5003, 1, 3400], [1, 0, 1], 136, 200, R, 2, seed=R), f"many rows R{R}")
+
+
+def test_one_adapter_of_many_holds_the_rows(w8):
+    """A pool so large that no adapter's rows are split: one workgroup passes
+    over more than 64 tiles, and the idle adapters' gradients are zero."""
+    t = Batch([64 * 70 + 5, 3], [77, 2], 128, 72, 16, 128, seed=1)
+    _check(w8, t, "128 adapters")
+
+
 @pytest.mark.parametrize("R,ranks", [(16, [16, 1, 0, 9]), (64, [64, 33, 8, 0]), (128, [100, 65, 64, 7]), (24, [99, -3, 17, 24])])
 def test_ranks_and_what_lies_beyond_them(w8, R, ranks):
     """Entries beyond an adapter's rank hold NaN and infinities; ranks outside

@@ -473,13 +473,16 @@ def gguf_a8_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
 
 
 # ------------------------------------------------------------------ adapters
+_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+
+
 def _view(t, rows, cols, dtype, device, name, align=True):
     """A matrix operand that may be a view with a row stride, never copied:
     (data pointer, row stride in elements).  `align`: rows must start on
     16-byte boundaries."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
@@ -502,7 +505,7 @@ def _vec(t, n, dtype, device, name):
     """A contiguous operand of at least n elements, or None: its pointer."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.device != device or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, on {device}, of at least {n} elements")
@@ -510,7 +513,7 @@ def _vec(t, n, dtype, device, name):
 
 
 def _gpu_matrix(t, name):
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -565,9 +568,9 @@ def _lora_args(rows, dev, a, b, plan, scale, ranks):
     if plan.rows != rows or plan.adapters != L or plan.device != dev:
         raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters on {plan.device}, "
                          f"the call has {rows} and {L} on {dev}")
-    pa = _vec(a, 0, torch.bfloat16, dev, "a")
-    pb = _vec(b, 0, torch.bfloat16, dev, "b")
-    return L, R, K, b.shape[1], pa, pb, _vec(scale, L, torch.float32, dev, "scale"), _vec(ranks, L, torch.int32, dev,
+    pa = _vec(a, 0, _BF16, dev, "a")
+    pb = _vec(b, 0, _BF16, dev, "b")
+    return L, R, K, b.shape[1], pa, pb, _vec(scale, L, _F32, dev, "scale"), _vec(ranks, L, _I32, dev,
                                                                                          "ranks")
 
 
@@ -579,14 +582,14 @@ def lora_forward(x, a, b, plan, scale=None, ranks=None, base=None, out=None, u=N
     dev = _gpu_matrix(x, "x")
     M = x.shape[0]
     L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
-    px, ldx = _view(x, M, K, torch.bfloat16, dev, "x")
-    pbase, ldbase = (None, 0) if base is None else _view(base, M, N, torch.bfloat16, dev, "base")
+    px, ldx = _view(x, M, K, _BF16, dev, "x")
+    pbase, ldbase = (None, 0) if base is None else _view(base, M, N, _BF16, dev, "base")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    po, ldo = _view(out, M, N, torch.bfloat16, dev, "out")
+        out = torch.empty((M, N), dtype=_BF16, device=dev)
+    po, ldo = _view(out, M, N, _BF16, dev, "out")
     if u is None and save_u:
-        u = torch.empty((M, R), dtype=torch.float32, device=dev)
-    pu = None if u is None else _vec(u, M * R, torch.float32, dev, "u")
+        u = torch.empty((M, R), dtype=_F32, device=dev)
+    pu = None if u is None else _vec(u, M * R, _F32, dev, "u")
     pws = None
     if u is None or workspace is not None:
         workspace = _buf(workspace, lora_forward_workspace_bytes(M, R), torch.uint8, dev, "workspace", alloc=16)
@@ -604,19 +607,19 @@ def lora_backward(dy, x, u, a, b, plan, scale=None, ranks=None, base=None, out=N
     dev = _gpu_matrix(dy, "dy")
     M = dy.shape[0]
     L, R, K, N, pa, pb, ps, pr = _lora_args(M, dev, a, b, plan, scale, ranks)
-    pdy, lddy = _view(dy, M, N, torch.bfloat16, dev, "dy")
-    px, ldx = _view(x, M, K, torch.bfloat16, dev, "x")
-    pu = _vec(u, M * R, torch.float32, dev, "u")
-    pbase, ldbase = (None, 0) if base is None else _view(base, M, K, torch.bfloat16, dev, "base")
+    pdy, lddy = _view(dy, M, N, _BF16, dev, "dy")
+    px, ldx = _view(x, M, K, _BF16, dev, "x")
+    pu = _vec(u, M * R, _F32, dev, "u")
+    pbase, ldbase = (None, 0) if base is None else _view(base, M, K, _BF16, dev, "base")
     dx, pdx, lddx = None, None, 0
     if need_dx:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if out is None else out
-        pdx, lddx = _view(dx, M, K, torch.bfloat16, dev, "out")
+        dx = _like(x) if out is None else out
+        pdx, lddx = _view(dx, M, K, _BF16, dev, "out")
     if need_weights:
         if u is None:
             raise ValueError("u, as lora_forward returned it, is needed for the weights' gradients")
-        da = _out(da, (L, R, K), torch.float32, dev, "da")
-        db = _out(db, (L, N, R), torch.float32, dev, "db")
+        da = _out(da, (L, R, K), _F32, dev, "da")
+        db = _out(db, (L, N, R), _F32, dev, "db")
     else:
         da = db = None
     ws = _buf(workspace, lora_backward_workspace_bytes(M, plan.tiles, K, N, R, L), torch.uint8, dev,
@@ -651,6 +654,11 @@ def _norm_args(x, weight, bias):
     return dev, M, K, xt, px, ldx, wt, pw, pb
 
 
+def _like(x):
+    """An uninitialized contiguous tensor of x's shape and type."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _first(t, n):
     return t if t.numel() == n else t[:n]
 
@@ -660,13 +668,13 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     or None.  Returns (y like x, mean f32 [M], rstd f32 [M])."""
     dev, M, K, xt, px, ldx, wt, pw, pb = _norm_args(x, weight, bias)
     if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=dev)
+        out = _like(x)
     py, ldy = _view(out, M, K, x.dtype, dev, "out", align=False)
     if mean is None:
-        mean = torch.empty(M, dtype=torch.float32, device=dev)
+        mean = torch.empty(M, dtype=_F32, device=dev)
     if rstd is None:
         rstd = torch.empty_like(mean)
-    pm, pr = _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd")
+    pm, pr = _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd")
     _check(_lib.layer_norm_forward(xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, pm, pr, _stream(dev)))
     return out, _first(mean, M), _first(rstd, M)
 
@@ -681,14 +689,14 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, dweight=None, 
     dbias f32 [K]), None for what is not needed (need_params: default, if there is a weight)."""
     dev, M, K, xt, px, ldx, wt, pw, _ = _norm_args(x, weight, None)
     pdy, lddy = _view(dy, M, K, x.dtype, dev, "dy", align=False)
-    pm, pr = _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd")
+    pm, pr = _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd")
     dx, pdx, lddx = None, None, 0
     if need_dx:
-        dx = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else out
+        dx = _like(x) if out is None else out
         pdx, lddx = _view(dx, M, K, x.dtype, dev, "out", align=False)
     if weight is not None if need_params is None else need_params:
-        dweight = _out(dweight, (K,), torch.float32, dev, "dweight")
-        dbias = _out(dbias, (K,), torch.float32, dev, "dbias")
+        dweight = _out(dweight, (K,), _F32, dev, "dweight")
+        dbias = torch.empty_like(dweight) if dbias is None else _out(dbias, (K,), _F32, dev, "dbias")
         ws = _buf(workspace, layer_norm_backward_workspace_bytes(M, K), torch.uint8, dev, "workspace", alloc=16)
         args = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
     else:
@@ -707,10 +715,10 @@ def w8a8_quant_act_rowwise_layer_norm(x, weight=None, bias=None, eps=1e-5, qtype
     ldq = ldq if ldq is not None else K + (-K) % 16
     xq = _out(out, (M, ldq), cd, dev, "out")
     if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        scale = torch.empty(M, dtype=_F32, device=dev)
     _check(_lib.w8a8_quant_act_rowwise_layer_norm(
-        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, _vec(scale, M, torch.float32, dev, "scale"),
-        _vec(mean, M, torch.float32, dev, "mean"), _vec(rstd, M, torch.float32, dev, "rstd"), _stream(dev)))
+        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, _vec(scale, M, _F32, dev, "scale"),
+        _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd"), _stream(dev)))
     return xq, _first(scale, M)
 
 

@@ -12,7 +12,12 @@
 //
 // All three are bound by streaming the wide tensors (x, dy, base, out): R is
 // small, so each takes 2 R operations for the 2 bytes of an element, far below
-// the 500 or so at which the matrix pipes would be the bound.
+// the 500 or so at which the matrix pipes would be the bound.  Measured (MI355X,
+// a large copy moves 5.3 TB/s; kernel times under rocprofv3, inputs rotated):
+//   M 8192, K 4096, N 12288, R 64, forward: down 26 us (67 MB of x; the rest is
+//   the weight, 512 KB a workgroup from L2), up 84 us (403 MB, 4.8 TB/s)
+//   M 8192, K = N 4096, R 32, backward: down 17 us (67 MB), up 30 us (134 MB,
+//   4.5 TB/s), outer sums 31 us (134 MB, 4.3 TB/s), their splits added up 4.5 us
 #include "block.hpp"
 
 namespace w8a8 {
@@ -233,7 +238,7 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
 // column i: a lane then holds 8 consecutive columns of a row, 16 lanes 256
 // bytes of it, and base (the sums' start) and out move as 16-byte accesses.
 // (The transposed product, 16 rows in 16 consecutive lanes, makes 64 requests
-// of each access: 99 us against %UP% at M 8192, C 12288, R 64.)  The workgroup
+// of each access: 99 us against 84 at M 8192, C 12288, R 64.)  The workgroup
 // turns v into two bf16 halves (hi + lo, ~16 bits) in LDS; up to R = 16 both
 // fit one 32-wide contraction, the weight twice.
 constexpr int kUpWaves = 4;
@@ -709,16 +714,17 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
 #undef W8A8_UP
 }
 
-// Whether the down- and the up-projection go in one launch: blocks of rows
-// times workgroups a block, and once more for the sums that each of a block's
-// workgroups repeats.  K = 4096, R = 16, one launch against two: 1 token and
-// 4096 columns 7.2 us against 7.8, 48 requests of one 7.6 against 8.6, 2039
-// tokens 13.8 against 15.0 (648); but 4096 tokens 34 against 21, 48 requests
-// and 12288 columns 16.7 against 10.5 (1836).  Ranks past 16 do not fit the
-// registers beside what is loaded ahead (32: 12.8 against 9.2 for 1 token).
+// Whether the down- and the up-projection go in one launch: where a workgroup
+// of it for each CU is enough (its registers leave room for one), and the sums
+// that each of a block's workgroups repeats do not add up.  K = 4096, R = 16,
+// one launch against two: 1 token and 4096 columns 7.2 us against 7.8, 48
+// requests of one 7.6 against 8.6, 1531 tokens and 2048 columns 8.5 against
+// 11.5; but 4096 tokens 34 against 21, 48 requests and 12288 columns 16.7
+// against 10.5.  Ranks past 16 do not fit the registers beside what is loaded
+// ahead (32: 12.8 against 9.2 for 1 token).
 bool one_launch(int64_t M, int64_t T, int64_t C2, int64_t R) {
-    const int64_t groups = (C2 + 2047) / 2048;
-    return R <= 16 && (M / 16 + T) * groups * groups <= 650;
+    const int64_t groups = (C2 + 2047) / 2048, blocks = (M / 16 + T) * groups;
+    return R <= 16 && blocks <= 256 && blocks * groups <= 512;
 }
 // out = base + (scale x w^T) w2^T; v [M, R] = scale x w^T is left where it is
 // not null (two launches need it).
@@ -870,7 +876,7 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga},
                                 {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb}};
         const int64_t grid = (ga + gb) * L * splits;
-        if (grid > INT32_MAX) return W8A8_ERR_SHAPE;
+        if (grid > INT32_MAX || (na + nb) / 1024 >= INT32_MAX) return W8A8_ERR_SHAPE;
 #define W8A8_OUTER(JB)                                                                                        \
     lora_outer_kernel<JB><<<(int)grid, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan,   \
                                                                      (int)T, (int)splits)
