@@ -151,11 +151,16 @@ __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x,
     // (8 XCDs: blocks 8 apart share an L2).
     const int turns = (slices + W - 1) / W;
     int turn = (int)((block / 8 + block) % (unsigned)turns);
-    v4u xd[RB][4], wd[kUnit];
+    // Weight blocks in flight: two for ranks past 64, whose 8 blocks a slice
+    // are most of the loads (R 128, M 8192, C 4096: 48 us with one, 34 with
+    // two; R 64: 23 and 24; a whole slice's, ahead of the next rows of x, 25).
+    constexpr int DW = JB == 8 && !TR ? 2 : 1;
+    v4u xd[RB][4], wd[DW][kUnit];
     int slice = turn * W + wave;
 #pragma unroll
     for (int a = 0; a < RB; ++a) fetch_x(slice, a, xd[a]);
-    fetch_w(slice, 0, wd);
+#pragma unroll
+    for (int q = 0; q < DW; ++q) fetch_w(slice, q, wd[q]);
     for (int n = 0; n < turns; ++n) {  // a slice past the end reads 0 without touching memory
         turn = turn + 1 < turns ? turn + 1 : 0;
         const int next = n + 1 < turns ? turn * W + wave : slices;
@@ -171,12 +176,12 @@ __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x,
         for (int q = 0; q < kUnits; ++q) {
             if constexpr (TR) {
 #pragma unroll
-                for (int i = 0; i < kUnit; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 16) = wd[i];
+                for (int i = 0; i < kUnit; ++i) *reinterpret_cast<v4u *>(area + (i * 64 + lane) * 16) = wd[q % DW][i];
             } else {
-                turn_in(area, wd, lane);
+                turn_in(area, wd[q % DW], lane);
             }
-            if (q + 1 < kUnits) fetch_w(slice, q + 1, wd);
-            else fetch_w(next, 0, wd);
+            if (q + DW < kUnits) fetch_w(slice, q + DW, wd[q % DW]);
+            else fetch_w(next, q + DW - kUnits, wd[q % DW]);
 #pragma unroll
             for (int i = 0; i < (TR ? JB : 4); ++i) {
                 const v4u f = TR ? transposed_fragment<JB>(area, i, lane) : turn_out(area, i, lane);
@@ -360,20 +365,53 @@ __device__ __forceinline__ void up_rows(const v4u (&bf)[4], const uint16_t (*hi)
     }
 }
 
+// The outer sums' splits, to be added up: da = sum of pa [splits][na], db of pb
+// (na, nb multiples of 4), 1024 elements a block of 256 threads.  With an input
+// gradient wanted too, these blocks go first in the up-projection's launch,
+// which hides their memory's latency (4.5 us as a launch of their own).
+struct SplitSums {
+    const float *pa, *pb;
+    float *da, *db;
+    int64_t na, nb;
+    int splits, blocks;
+};
+__device__ __forceinline__ void add_splits(const SplitSums &sums, int block) {
+    int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4;
+    const bool is_a = i < sums.na;
+    const float *p = is_a ? sums.pa : sums.pb;
+    float *d = is_a ? sums.da : sums.db;
+    const int64_t n = is_a ? sums.na : sums.nb;
+    if (!is_a) i -= sums.na;
+    if (i >= n) return;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < sums.splits; k += 8) {
+        v4f q[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            q[c] = k + c < sums.splits ? *reinterpret_cast<const v4f *>(p + (k + c) * n + i) : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s += q[c];
+    }
+    *reinterpret_cast<v4f *>(d + i) = s;
+}
+
 template <int JB, bool TR>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
                                                                 int L, int R, const int32_t *ranks,
                                                                 const int32_t *plan, int groups, const uint16_t *base,
-                                                                int64_t ldbase, uint16_t *out, int64_t ldout) {
+                                                                int64_t ldbase, uint16_t *out, int64_t ldout,
+                                                                SplitSums sums) {
+    if ((int)blockIdx.x < sums.blocks) return add_splits(sums, blockIdx.x);
+    const int block = blockIdx.x - sums.blocks;
     constexpr int KB = JB == 1 ? 1 : JB / 2;  // 32-wide contractions
     constexpr int RB = kTileRows / 16;
     constexpr int P = JB * 16 + 8;  // halves of an LDS row: 16 rows' reads fall on distinct banks
     __shared__ __attribute__((aligned(16))) uint16_t vs[2][kTileRows][P];
     __shared__ __attribute__((aligned(16))) char ws[TR ? 1 : kUpWaves][TR ? 16 : JB == 1 ? 4096 : 8192];
-    const Tile tile = load_tile(plan, blockIdx.x / groups, M, L);
+    const Tile tile = load_tile(plan, block / groups, M, L);
     if (tile.rows == 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col0 = (blockIdx.x % groups * kUpWaves + wave) * 128;
+    const int col0 = (block % groups * kUpWaves + wave) * 128;
     const auto rv = v_rsrc(v, tile.row0, tile.rows, R);
     constexpr int kChunks = kTileRows * JB * 4 / (64 * kUpWaves);  // 4-float chunks of v per thread
     v4u vd[kChunks];
@@ -654,25 +692,7 @@ __global__ __launch_bounds__(64 * kOuterWaves) void lora_outer_kernel(OuterPair 
     else outer_block<JB, false>(both.b, q - na, M, L, R, ranks, plan, T, splits, ys, vs);
 }
 
-// da = sum of its splits [splits][na], db likewise (na, nb multiples of 4).
-__global__ __launch_bounds__(256) void lora_reduce_kernel(const float *pa, int64_t na, float *da, const float *pb,
-                                                          int64_t nb, float *db, int splits) {
-    int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    const float *p = pa;
-    float *d = da;
-    int64_t n = na;
-    if (i >= na) i -= na, p = pb, d = db, n = nb;
-    if (i >= n) return;
-    v4f s = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < splits; k += 8) {
-        v4f q[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) q[c] = k + c < splits ? *reinterpret_cast<const v4f *>(p + (k + c) * n + i) : v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 8; ++c) s += q[c];
-    }
-    *reinterpret_cast<v4f *>(d + i) = s;
-}
+__global__ __launch_bounds__(256) void lora_sums_kernel(SplitSums sums) { add_splits(sums, blockIdx.x); }
 
 // ---------------------------------------------------------------- host side
 int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
@@ -700,11 +720,11 @@ void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uin
 template <bool TR>
 void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t L, int64_t R, const int32_t *ranks,
                const int32_t *plan, int64_t T, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout,
-               hipStream_t stream) {
+               const SplitSums &sums, hipStream_t stream) {
     const int groups = (int)((C + 128 * kUpWaves - 1) / (128 * kUpWaves));
 #define W8A8_UP(JB)                                                                                                  \
-    lora_up_kernel<JB, TR><<<(int)(T * groups), 64 * kUpWaves, 0, stream>>>(v, w, M, (int)C, (int)L, (int)R, ranks,   \
-                                                                            plan, groups, base, ldbase, out, ldout)
+    lora_up_kernel<JB, TR><<<(int)(T * groups) + sums.blocks, 64 * kUpWaves, 0, stream>>>(                            \
+        v, w, M, (int)C, (int)L, (int)R, ranks, plan, groups, base, ldbase, out, ldout, sums)
     switch (rank_blocks(R)) {
     case 1: W8A8_UP(1); break;
     case 2: W8A8_UP(2); break;
@@ -726,20 +746,15 @@ bool one_launch(int64_t M, int64_t T, int64_t C2, int64_t R) {
     const int64_t groups = (C2 + 2047) / 2048, blocks = (M / 16 + T) * groups;
     return R <= 16 && blocks <= 256 && blocks * groups <= 512;
 }
-// out = base + (scale x w^T) w2^T; v [M, R] = scale x w^T is left where it is
-// not null (two launches need it).
+// out = base + (scale x w^T) w2^T; v [M, R] = scale x w^T is left where it is not null.
 template <bool TR>
 void both_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uint16_t *w, int64_t L, int64_t R,
                  const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T, float *v, const uint16_t *w2,
                  int64_t C2, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout, hipStream_t stream) {
-    if (one_launch(M, T, C2, R)) {
-        const int groups = (int)((C2 + 2047) / 2048);
-        lora_both_kernel<TR><<<(int)(4 * T * groups), 1024, 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, ranks, plan, (int)T, v, w2,
-                                                           (int)C2, groups, base, ldbase, out, ldout);
-        return;
-    }
-    down_launch<TR>(x, M, C, ldx, w, L, R, scale, ranks, plan, T, v, stream);
-    up_launch<TR>(v, w2, M, C2, L, R, ranks, plan, T, base, ldbase, out, ldout, stream);
+    const int groups = (int)((C2 + 2047) / 2048);
+    lora_both_kernel<TR><<<(int)(4 * T * groups), 1024, 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, ranks,
+                                                                     plan, (int)T, v, w2, (int)C2, groups, base, ldbase,
+                                                                     out, ldout);
 }
 
 // Over how many workgroups an adapter's rows are split.  Each split's sums are
@@ -837,7 +852,12 @@ extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int
     if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(u) || !aligned16(workspace))
         return W8A8_ERR_ALIGN;
     float *v = u ? u : static_cast<float *>(workspace);
-    both_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, b, N, base, ldbase, out, ldout, stream);
+    if (one_launch(M, T, N, R)) {
+        both_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, b, N, base, ldbase, out, ldout, stream);
+    } else {
+        down_launch<false>(x, M, K, ldx, a, L, R, scale, ranks, plan, T, v, stream);
+        up_launch<false>(v, b, M, N, L, R, ranks, plan, T, base, ldbase, out, ldout, SplitSums{}, stream);
+    }
     return launch_status();
 }
 
@@ -866,17 +886,23 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         !aligned16(db) || !aligned16(workspace))
         return W8A8_ERR_ALIGN;
     float *g = static_cast<float *>(workspace), *parts = g + M * R;
-    if (T > 0) {
-        if (dx) both_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, a, K, base, ldbase, dx, lddx, stream);
-        else down_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, stream);
+    const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
+    const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
+    const int64_t grid = (ga + gb) * L * splits;
+    if (da && (grid > INT32_MAX || (na + nb) / 1024 >= INT32_MAX / 2)) return W8A8_ERR_SHAPE;
+    SplitSums sums = {};
+    if (da && splits > 1) {
+        sums = {parts, parts + splits * na, da, db, na, nb, (int)splits, (int)(((na + nb) / 4 + 255) / 256)};
+        if (sums.blocks + T * ((K + 511) / 512) > INT32_MAX) return W8A8_ERR_SHAPE;
     }
+    // dx in one launch with g where that fits; else after the outer sums, whose
+    // splits its launch adds up
+    const bool one = T > 0 && dx && one_launch(M, T, K, R);
+    if (one) both_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, a, K, base, ldbase, dx, lddx, stream);
+    else if (T > 0) down_launch<true>(dy, M, N, lddy, b, L, R, scale, ranks, plan, T, g, stream);
     if (da) {
-        const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
-        const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
         const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga},
                                 {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb}};
-        const int64_t grid = (ga + gb) * L * splits;
-        if (grid > INT32_MAX || (na + nb) / 1024 >= INT32_MAX) return W8A8_ERR_SHAPE;
 #define W8A8_OUTER(JB)                                                                                        \
     lora_outer_kernel<JB><<<(int)grid, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan,   \
                                                                      (int)T, (int)splits)
@@ -887,9 +913,10 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         default: W8A8_OUTER(8); break;
         }
 #undef W8A8_OUTER
-        if (splits > 1)
-            lora_reduce_kernel<<<(int)(((na + nb) / 4 + 255) / 256), 256, 0, stream>>>(parts, na, da, parts + splits * na, nb,
-                                                                                      db, (int)splits);
     }
+    if (T > 0 && dx && !one)
+        up_launch<true>(g, a, M, K, L, R, ranks, plan, T, base, ldbase, dx, lddx, sums, stream);
+    else if (sums.blocks > 0)
+        lora_sums_kernel<<<sums.blocks, 256, 0, stream>>>(sums);
     return launch_status();
 }
