@@ -757,15 +757,15 @@ void both_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uin
                                                                      out, ldout);
 }
 
-// Over how many workgroups an adapter's rows are split.  Each split's sums are
-// written and read again (with the launch that adds them up), so one workgroup
-// for each CU is enough; from R = 64 on a workgroup's products and LDS reads
-// take as long as its loads, and two for each CU overlap them.  Both
-// gradients, with the down-projection, M 8192, K = N 4096, 1, 4, 8, 16 splits:
-// R 32 112, 45, 45, 46 us; R 64 169, 63, 56, 64 us.
-int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
+// Over how many workgroups an adapter's rows are split: two workgroups for each
+// CU, which overlap each other's loads, products and barriers, and no more,
+// since each split's sums are written and read again.  Both gradients, with
+// the down-projection, M 8192, K = N 4096, 1, 4, 8, 16 splits: R 32 116, 50,
+// 51, 52 us; R 64 173, 68, 64, 73 us.  2039 rows of 4 adapters, K 4096, N 1024,
+// R 16, the sums' kernel alone: 15.6 us with 1 split, 11.0 with 3.
+int64_t outer_splits(int64_t T, int64_t K, int64_t N, int64_t L) {
     const int64_t one = ((K + 127) / 128 + (N + 127) / 128) * L, most = T / (2 * L);
-    const int64_t s = (R <= 32 ? 256 : 512) / one;
+    const int64_t s = 512 / one;
     return s < most ? (s < 1 ? 1 : s) : most < 1 ? 1 : most;
 }
 
@@ -864,7 +864,7 @@ extern "C" w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int
 extern "C" size_t lora_backward_workspace_bytes(int64_t M, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
     using namespace w8a8;
     if (M < 0 || T < 0 || K < 8 || N < 8 || L < 1 || R < 8 || R > kMaxR) return 0;
-    const int64_t splits = outer_splits(T, K, N, R, L);
+    const int64_t splits = outer_splits(T, K, N, L);
     return (size_t)(M * R + (splits > 1 ? splits * L * R * (K + N) : 0)) * sizeof(float);
 }
 
@@ -886,7 +886,7 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
         !aligned16(db) || !aligned16(workspace))
         return W8A8_ERR_ALIGN;
     float *g = static_cast<float *>(workspace), *parts = g + M * R;
-    const int64_t splits = outer_splits(T, K, N, R, L), na = L * R * K, nb = L * R * N;
+    const int64_t splits = outer_splits(T, K, N, L), na = L * R * K, nb = L * R * N;
     const int ga = (int)((K + 127) / 128), gb = (int)((N + 127) / 128);
     const int64_t grid = (ga + gb) * L * splits;
     if (da && (grid > INT32_MAX || (na + nb) / 1024 >= INT32_MAX / 2)) return W8A8_ERR_SHAPE;
