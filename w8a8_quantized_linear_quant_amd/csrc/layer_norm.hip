@@ -77,8 +77,11 @@ __device__ __forceinline__ uint32_t codes4(const float *v, float s, float r) {
 // ---------------------------------------------------------------- resident
 // Rows that fit the registers of one workgroup are read once: W waves share a
 // row, thread t of the row's 64 W holds its chunks t, t + 64 W, ... (16 bytes
-// each).  A workgroup takes `rows` rows (of each of its row groups), the next
-// row's loads in flight while a row is worked on, the weights in registers.
+// each).  A workgroup takes several rows, the next one's loads in flight while a
+// row is worked on, the weights in registers.  Bound by memory in f32 (8192
+// rows of 4096: 48 us, 5.6 TB/s with what the caches keep) and nearly so in bf16
+// (25.6 us, 5.2 TB/s); to codes by memory and about 25 vector instructions an
+// element alike (22.9 us, 4.4 TB/s).
 // OUT: what leaves (the norm in X's type, int8 codes or e4m3 codes).  EVEN: K
 // is a whole number of chunks, so that a chunk is either there or not.
 enum { kOutNorm = 0, kOutInt8 = 1, kOutE4m3 = 2 };
@@ -109,7 +112,8 @@ __device__ __forceinline__ ParamChunk<WT, VEC> fetch_params(const void *p, int c
     if constexpr (EVEN) {
         if constexpr (WT == W8A8_F32) {
 #pragma unroll
-            for (int i = 0; i < VEC / 4; ++i) c.d[i] = *reinterpret_cast<const v4u *>(static_cast<const float *>(p) + col + 4 * i);
+            for (int i = 0; i < VEC / 4; ++i)
+                c.d[i] = *reinterpret_cast<const v4u *>(static_cast<const float *>(p) + col + 4 * i);
         } else if constexpr (VEC == 8) {
             c.d[0] = *reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(p) + col);
         } else {
@@ -207,7 +211,7 @@ __global__ __launch_bounds__(kResidentThreads<W>) void ln_resident_kernel(const 
     __shared__ float top_part[2][G][W];
     const int group = threadIdx.x / T, tid = threadIdx.x % T;
     const int64_t step = (int64_t)gridDim.x * G;
-    float counts[W];  // never 0: mean_w = 0 / 1 for a wave without elements
+    float counts[W];  // a wave without elements has count 0 and takes 0 / 1 for its mean
 #pragma unroll
     for (int k = 0; k < W; ++k) counts[k] = (float)wave_elements<V, W>(K, k);
     const float own_n = fmaxf((float)wave_elements<V, W>(K, tid >> 6), 1.f);
@@ -341,8 +345,8 @@ constexpr int backward_threads(int ept) { return ept <= 8 ? 1024 : 512; }
 
 // As the forward kernel, and each thread keeps the sums over its workgroup's
 // rows of dy h and dy for its own columns.  A workgroup of `groups` row groups
-// takes every gridDim.x * groups-th row; the next row's loads are in flight
-// while a row is worked on.  At the end the groups' sums meet in LDS and leave
+// takes every gridDim.x * groups-th row (8192 x 4096 bf16: 38 us for 201 MB, 5 TB/s);
+// the next row's loads are in flight while a row is worked on.  At the end the groups' sums meet in LDS and leave
 // as partials [workgroup][dw, db][position]; ln_reduce_kernel adds them.
 // Position p of column c = (i T + t) V + e:  p = (i V + e) T + t.
 template <class X, int WT, bool EVEN, int W, int NCH, bool PARAMS>
@@ -449,31 +453,30 @@ __global__ __launch_bounds__(backward_threads(NCH * X::kVec)) void ln_backward_k
     }
 }
 
-// dw and db from `count` partials [2][positions]: 16 positions a workgroup, the
-// partials split over its 64 threads for each.  T = 0: position = column.
+// dw and db from `count` partials [2][positions]: 32 positions a workgroup, the
+// partials split over its 32 threads for each.  T = 0: position = column.
 __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float *partials, int count, int64_t positions, int T,
                                                          int V, int K, float *dw, float *db) {
-    __shared__ float part[64][17];
-    const int lane = threadIdx.x & 15, split = threadIdx.x >> 4;
-    const int64_t p = (int64_t)blockIdx.x * 16 + lane;
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, split = threadIdx.x >> 5;
+    const int64_t p = (int64_t)blockIdx.x * 32 + lane;
     float a = 0.f;
     if (p < 2 * positions) {
-        float v[kMaxGroups / 64];
+        float v[kMaxGroups / 32];
 #pragma unroll
-        for (int i = 0; i < kMaxGroups / 64; ++i) {
-            const int g = split + 64 * i;
+        for (int i = 0; i < kMaxGroups / 32; ++i) {
+            const int g = split + 32 * i;
             v[i] = g < count ? partials[g * 2 * positions + p] : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kMaxGroups / 64; ++i) a += v[i];
+        for (int i = 0; i < kMaxGroups / 32; ++i) a += v[i];
     }
     part[split][lane] = a;
     __syncthreads();
     if (threadIdx.x >= 64) return;
     a = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) a += part[split + 4 * k][lane];
-    a += __shfl_xor(a, 16);
+    for (int k = 0; k < 16; ++k) a += part[split * 16 + k][lane];
     a += __shfl_xor(a, 32);
     if (split != 0 || p >= 2 * positions) return;
     const int64_t q = p < positions ? p : p - positions;
@@ -551,9 +554,10 @@ Layout forward_layout(int64_t K) {
 }
 // Backward with the parameters' sums: 8 elements per thread, whose sums, rows
 // in flight and weights fit 128 registers, 16 waves to a CU (8192 rows of 4096
-// bf16: 44.0 us; 16 elements and 8 waves to a CU: 45.1).
+// bf16: 43 us; 16 elements and 8 waves to a CU: 45).  5 waves fill widths a
+// little past 2048 (2560: 30 us, 37 with 8).
 Layout backward_layout(int64_t K) {
-    for (int W = 1; W <= 16; W *= 2)
+    for (int W : {1, 2, 4, 5, 8, 16})
         if (K <= 64 * W * 8) return {W, 8};
     return {0, 0};
 }
@@ -571,8 +575,7 @@ Layout backward_dx_layout(int64_t K) {
 void backward_grid(int64_t M, Layout lay, int &groups, int &count) {
     const int most = backward_threads(lay.ept) / (64 * lay.W);
     const int64_t per = (M + kMaxGroups - 1) / kMaxGroups;
-    groups = 1;
-    while (groups < per && groups < most) groups *= 2;
+    groups = (int)(per < 1 ? 1 : per < most ? per : most);
     const int64_t n = (M + groups - 1) / groups;
     count = (int)(n < kMaxGroups ? (n < 1 ? 1 : n) : kMaxGroups);
 }
@@ -675,7 +678,7 @@ w8a8_status backward_launch(const BackwardArgs &a, hipStream_t stream) {
         positions = (int64_t)T * lay.ept;
 #define W8A8_LN(W_) \
     if (lay.W == W_) backward_resident<X, W_, 8, true>(a, count, groups, stream);
-        W8A8_LN(1) W8A8_LN(2) W8A8_LN(4) W8A8_LN(8) W8A8_LN(16)
+        W8A8_LN(1) W8A8_LN(2) W8A8_LN(4) W8A8_LN(5) W8A8_LN(8) W8A8_LN(16)
 #undef W8A8_LN
     } else {
         // the parameters' sums first: dx may be dy
@@ -686,7 +689,7 @@ w8a8_status backward_launch(const BackwardArgs &a, hipStream_t stream) {
     }
     const w8a8_status st = launch_status();
     if (st != W8A8_OK) return st;
-    ln_reduce_kernel<<<(int)((2 * positions + 15) / 16), 1024, 0, stream>>>(a.partials, count, positions, T, X::kVec, a.K,
+    ln_reduce_kernel<<<(int)((2 * positions + 31) / 32), 1024, 0, stream>>>(a.partials, count, positions, T, X::kVec, a.K,
                                                                            a.dweight, a.dbias);
     return launch_status();
 }
