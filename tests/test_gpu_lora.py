@@ -141,6 +141,12 @@ def test_many_rows(w8, R):
     _check(w8, Batch([5003, 1, 3400], [1, 0, 1], 136, 200, R, 2, seed=R), f"many rows R{R}")
 
 
+@pytest.mark.parametrize("M,R", [(200, 64), (1000, 128), (3000, 32), (3000, 64), (3000, 128)])
+def test_middling_rows(w8, M, R):
+    """Ranks in parts, fewer and none, at 16 rows a workgroup."""
+    _check(w8, Batch([M - 7, 7], [1, 0], 264, 520, R, 2, seed=M + R), f"{M} rows R{R}")
+
+
 def test_one_adapter_of_many_holds_the_rows(w8):
     """A pool so large that no adapter's rows are split: one workgroup passes
     over more than 64 tiles, and the idle adapters' gradients are zero."""

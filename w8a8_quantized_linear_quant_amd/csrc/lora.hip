@@ -113,11 +113,11 @@ __device__ __forceinline__ v4u transposed_fragment(const char *area, int jb, int
 }
 
 // acc += this wave's slices of rows x weight, for the 16 RB rows from `first`
-// of a tile; area: the wave's LDS; block: which workgroup asks (all that share
+// of a tile and the 16 JB ranks from j0; area: the wave's LDS; block: which workgroup asks (all that share
 // a result must give the same, for the order of its sums).
 template <int JB, int RB, bool TR, int W>
 __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x, const Tile &tile, int first, int C,
-                                          int64_t ldx, const uint16_t *w, int R, char *area, unsigned block) {
+                                          int64_t ldx, const uint16_t *w, int R, int j0, char *area, unsigned block) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int slices = (C + kSlice - 1) / kSlice;
     if (wave >= slices) return;
@@ -137,11 +137,12 @@ __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x,
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
             if constexpr (TR) {  // 32 rows n of a step, all ranks
-                const int c = i * 64 + lane, row = slice * kSlice + unit * 32 + c / (2 * JB), j = c % (2 * JB) * 8;
+                const int c = i * 64 + lane, row = slice * kSlice + unit * 32 + c / (2 * JB);
+                const int j = j0 + c % (2 * JB) * 8;
                 d[i] = load16(rw, row < C && j < R ? (row * R + j) * 2 : kOobOffset);
             } else {             // 16 ranks of a slice
                 const int k = slice * kSlice + lc;
-                d[i] = load16(rw, k < C ? ((unit * 16 + i * 4 + li) * C + k) * 2 : kOobOffset);
+                d[i] = load16(rw, k < C ? ((j0 + unit * 16 + i * 4 + li) * C + k) * 2 : kOobOffset);
             }
         }
     };
@@ -199,15 +200,16 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
                                                                             int64_t ldx, const uint16_t *w, int L,
                                                                             int R, const float *scale,
                                                                             const int32_t *ranks, const int32_t *plan,
-                                                                            int T, float *v) {
+                                                                            int T, int j_parts, float *v) {
     constexpr int W = down_waves(JB, RB);
     constexpr int kArea = TR && JB > 4 ? JB * 1024 : 4096;  // bytes of a wave
     constexpr int kSums = W * RB * 16 * 17 * 4;
     __shared__ __attribute__((aligned(16))) char lds[W * kArea > kSums ? W * kArea : kSums];
     // the tiles' first parts come first: short tiles have no others, and the
     // blocks that are left must not fall on the same few XCDs
-    const Tile tile = load_tile(plan, blockIdx.x % T, M, L);
-    const int first = blockIdx.x / T * (16 * RB);
+    const int block = blockIdx.x / j_parts, j0 = blockIdx.x % j_parts * (16 * JB);
+    const Tile tile = load_tile(plan, block % T, M, L);
+    const int first = block / T * (16 * RB);
     if (first >= tile.rows) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = rank_of(ranks, tile.adapter, R);
@@ -217,7 +219,8 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
     for (int a = 0; a < RB; ++a)
 #pragma unroll
         for (int b = 0; b < JB; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (r > 0) down_sums<JB, RB, TR, W>(acc, x, tile, first, C, ldx, w, R, lds + wave * kArea, blockIdx.x);
+    // (the rank masks what is written; no load waits for it)
+    if (tile.adapter >= 0) down_sums<JB, RB, TR, W>(acc, x, tile, first, C, ldx, w, R, j0, lds + wave * kArea, blockIdx.x);
     auto part = reinterpret_cast<float (*)[RB * 16][17]>(lds);
 #pragma unroll
     for (int b = 0; b < JB; ++b) {
@@ -227,7 +230,7 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; ++e) part[wave][a * 16 + 4 * (lane >> 4) + e][lane & 15] = acc[a][b][e];
         __syncthreads();
-        const int row = threadIdx.x / 16, j = b * 16 + threadIdx.x % 16;
+        const int row = threadIdx.x / 16, j = j0 + b * 16 + threadIdx.x % 16;
         if (row < RB * 16 && first + row < tile.rows && j < R) {
             float t = 0.f;
 #pragma unroll
@@ -395,25 +398,28 @@ __device__ __forceinline__ void add_splits(const SplitSums &sums, int block) {
     *reinterpret_cast<v4f *>(d + i) = s;
 }
 
-template <int JB, bool TR>
+template <int JB, bool TR, int RB>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
                                                                 int L, int R, const int32_t *ranks,
                                                                 const int32_t *plan, int groups, const uint16_t *base,
                                                                 int64_t ldbase, uint16_t *out, int64_t ldout,
                                                                 SplitSums sums) {
     if ((int)blockIdx.x < sums.blocks) return add_splits(sums, blockIdx.x);
-    const int block = blockIdx.x - sums.blocks;
     constexpr int KB = JB == 1 ? 1 : JB / 2;  // 32-wide contractions
-    constexpr int RB = kTileRows / 16;
     constexpr int P = JB * 16 + 8;  // halves of an LDS row: 16 rows' reads fall on distinct banks
-    __shared__ __attribute__((aligned(16))) uint16_t vs[2][kTileRows][P];
+    constexpr int kRows = 16 * RB, kParts = kTileRows / kRows;
+    __shared__ __attribute__((aligned(16))) uint16_t vs[2][kRows][P];
     __shared__ __attribute__((aligned(16))) char ws[TR ? 1 : kUpWaves][TR ? 16 : JB == 1 ? 4096 : 8192];
-    const Tile tile = load_tile(plan, block / groups, M, L);
-    if (tile.rows == 0) return;
+    // blocks of a tile's rows: columns, then its next 16 RB rows
+    const int block = blockIdx.x - sums.blocks, part = block / groups;
+    Tile tile = load_tile(plan, part / kParts, M, L);
+    tile.row0 += part % kParts * kRows;
+    tile.rows = min(tile.rows - part % kParts * kRows, kRows);
+    if (tile.rows <= 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col0 = (block % groups * kUpWaves + wave) * 128;
     const auto rv = v_rsrc(v, tile.row0, tile.rows, R);
-    constexpr int kChunks = kTileRows * JB * 4 / (64 * kUpWaves);  // 4-float chunks of v per thread
+    constexpr int kChunks = (kRows * JB * 4 + 64 * kUpWaves - 1) / (64 * kUpWaves);  // 4-float chunks of v per thread
     v4u vd[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -444,6 +450,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int q = i * 64 * kUpWaves + threadIdx.x, row = q / (JB * 4), j = q % (JB * 4) * 4;
+        if (row >= kRows) break;
         uint2 hi, lo;
         split2(__builtin_bit_cast(v4f, vd[i]), hi, lo);
         *reinterpret_cast<uint2 *>(&vs[0][row][j]) = hi;
@@ -492,7 +499,7 @@ __global__ __launch_bounds__(1024) void lora_both_kernel(const uint16_t *x, int6
     v4f acc[1][JB];
 #pragma unroll
     for (int b = 0; b < JB; ++b) acc[0][b] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (r > 0) down_sums<JB, 1, TR, W>(acc, x, tile, first, C, ldx, w, R, lds + wave * kArea, block);
+    if (tile.adapter >= 0) down_sums<JB, 1, TR, W>(acc, x, tile, first, C, ldx, w, R, 0, lds + wave * kArea, block);
     auto part = reinterpret_cast<float (*)[16][17]>(lds);
 #pragma unroll
     for (int b = 0; b < JB; ++b) {
@@ -591,8 +598,7 @@ __device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, in
     const int r = rank_of(ranks, l, R);
     const int32_t *first = plan + 4 * (int64_t)T;
     const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
-    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits);
-    const int end = r > 0 ? t0 + (int)((int64_t)n * (split + 1) / splits) : begin;
+    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits), end = t0 + (int)((int64_t)n * (split + 1) / splits);
     v4f acc[NC][NJ];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -701,14 +707,21 @@ int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8;
 template <bool TR>
 void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uint16_t *w, int64_t L, int64_t R,
                  const float *scale, const int32_t *ranks, const int32_t *plan, int64_t T, float *v, hipStream_t stream) {
-    // 32 rows a workgroup read the weights half as often; 16 where that would
-    // leave CUs idle
-    const bool two = 2 * T >= 256;
-    const int grid = (int)(two ? 2 * T : 4 * T);
-#define W8A8_DOWN(JB, RB)                                                                                          \
-    lora_down_kernel<JB, RB, TR><<<grid, 64 * down_waves(JB, RB), 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R, scale, \
-                                                                       ranks, plan, (int)T, v)
-    switch (rank_blocks(R)) {
+    // 16 rows a workgroup while those are no more than one to a CU, of which
+    // mostly one fits a CU; else 32, which read the weights half as often
+    // (C 4096, R 16 and 128: 4096 rows 14.3 and 27.5 us with 16, 14.4 and 30.2
+    // with 32; 4500 rows 19.0 and 41.7, 15.7 and 32.3)
+    const bool two = M > 16 * 256;
+    // fewer still: the ranks in parts, since one CU takes long for a weight of
+    // many (1 row, C 4096, R 128, with the up-projection: 19.2 us, 9.9 in 8 parts)
+    int blocks = rank_blocks(R), parts = 1;
+    if (!two)
+        while (blocks > 1 && (M / 16 + T) * parts * 2 <= 256) blocks /= 2, parts *= 2;
+    const int grid = (int)(two ? 2 * T : 4 * T) * parts;
+#define W8A8_DOWN(JB, RB)                                                                                              \
+    lora_down_kernel<JB, RB, TR><<<grid, 64 * down_waves(JB, RB), 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R,   \
+                                                                              scale, ranks, plan, (int)T, parts, v)
+    switch (blocks) {
     case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
     case 2: two ? W8A8_DOWN(2, 2) : W8A8_DOWN(2, 1); break;
     case 4: two ? W8A8_DOWN(4, 2) : W8A8_DOWN(4, 1); break;
@@ -722,14 +735,19 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
                const int32_t *plan, int64_t T, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout,
                const SplitSums &sums, hipStream_t stream) {
     const int groups = (int)((C + 128 * kUpWaves - 1) / (128 * kUpWaves));
-#define W8A8_UP(JB)                                                                                                  \
-    lora_up_kernel<JB, TR><<<(int)(T * groups) + sums.blocks, 64 * kUpWaves, 0, stream>>>(                            \
-        v, w, M, (int)C, (int)L, (int)R, ranks, plan, groups, base, ldbase, out, ldout, sums)
+    // 64 rows a workgroup use the weights' fragments most often; 32 where that
+    // would leave less than two workgroups to a CU (300 rows, K 2048, N 5120, R
+    // 32, both launches: 9.3 us against 10.5)
+    const bool half = T * groups < 512;
+    const int grid = (int)(T * groups) * (half ? 2 : 1) + sums.blocks;
+#define W8A8_UP(JB, RB)                                                                                          \
+    lora_up_kernel<JB, TR, RB><<<grid, 64 * kUpWaves, 0, stream>>>(v, w, M, (int)C, (int)L, (int)R, ranks, plan, \
+                                                                   groups, base, ldbase, out, ldout, sums)
     switch (rank_blocks(R)) {
-    case 1: W8A8_UP(1); break;
-    case 2: W8A8_UP(2); break;
-    case 4: W8A8_UP(4); break;
-    default: W8A8_UP(8); break;
+    case 1: half ? W8A8_UP(1, 2) : W8A8_UP(1, 4); break;
+    case 2: half ? W8A8_UP(2, 2) : W8A8_UP(2, 4); break;
+    case 4: half ? W8A8_UP(4, 2) : W8A8_UP(4, 4); break;
+    default: half ? W8A8_UP(8, 2) : W8A8_UP(8, 4); break;
     }
 #undef W8A8_UP
 }
