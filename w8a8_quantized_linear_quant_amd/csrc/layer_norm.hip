@@ -159,11 +159,20 @@ template <class X, int W, int NCH, bool EVEN>
 __device__ __forceinline__ void resident_stats(const float (&v)[NCH][X::kVec], int K, int tid, float own_n, float eps,
                                                const float *counts, float2 *part, float &mean, float &rstd) {
     constexpr int V = X::kVec, T = 64 * W;
+    // chunk by chunk in pairs: fewer roundings on each element's way than one
+    // running sum, which counts where the mean is near 0
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
+    for (int i = 0; i < NCH; ++i) {
+        float c[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += v[i][e];
+        for (int e = 0; e < V; ++e) c[e] = v[i][e];
+#pragma unroll
+        for (int h = V / 2; h > 0; h /= 2)
+#pragma unroll
+            for (int e = 0; e < h; ++e) c[e] += c[e + h];
+        s += c[0];
+    }
     const float mu = wave_sum(s) / own_n;
     float q = 0.f;
 #pragma unroll
