@@ -140,7 +140,10 @@ w8a8_status layer_norm_backward(w8a8_dtype xt, const void *dy, int64_t lddy, con
 /*
  * Row-wise activation quantization (w8a8_quant_act_rowwise) of the rows'
  * layer norm, in one pass: the shared absmax rule on the f32 values of y
- * (never rounded to bf16).
+ * (never rounded to bf16).  A NaN in a row's y makes its absmax and so its
+ * scale NaN, e4m3's codes too; beside an infinite scale e4m3's codes are zeros
+ * of y's signs, NaN where y is infinite.  int8 codes are 0 beside a scale that
+ * is not finite (a product with either is NaN).
  *   x [M, ldx] of type xt; weight, bias, eps, mean, rstd as
  *   layer_norm_forward; xq codes [M, ldq], columns K .. ldq - 1 written as
  *   zero; x_scale f32 [M].

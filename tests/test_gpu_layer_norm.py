@@ -374,3 +374,60 @@ def test_binding_refusals(w8):
     for kw in (dict(qtype=3), dict(ldq=80, out=torch.empty(8, 64, dtype=torch.int8).cuda()), dict(scale=mu[:3])):
         with pytest.raises((TypeError, ValueError)):
             w8.w8a8_quant_act_rowwise_layer_norm(x, w, b, **kw)
+
+
+# ------------------------------------------------- non-finite rows to codes
+CODE_K = [40, 520, 1001, 4096, 4100, 16384, 17000]     # one wave, several, both sides of the streamed rows
+
+
+@pytest.mark.parametrize("qt", [0, 1])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", CODE_K)
+def test_codes_keep_nan_and_infinity(w8, qt, xt, K):
+    """A NaN or an infinity in x makes the whole norm of its row NaN: the
+    absmax and so the scale are NaN, and so are e4m3's codes (int8 has none:
+    0).  The other rows' bits do not change, columns past K stay zero, and a
+    product with such a row is NaN, not the bias."""
+    print(f"[norm] non-finite codes qt={qt} {xt} K{K}", flush=True)
+    M = 9
+    x, _, w, b = _inputs(M, K, xt, "f32", seed=K)
+    cq, cs = w8.w8a8_quant_act_rowwise_layer_norm(x.cuda(), w.cuda(), b.cuda(), qtype=qt)
+    x[4, K - 1], x[6, K // 2], x[7, 3] = float("nan"), float("-inf"), float("inf")
+    xq, sx = w8.w8a8_quant_act_rowwise_layer_norm(x.cuda(), w.cuda(), b.cuda(), qtype=qt)
+    keep, gone = [0, 1, 2, 3, 5, 8], [4, 6, 7]
+    assert torch.equal(xq[keep].view(torch.uint8), cq[keep].view(torch.uint8)) and torch.equal(sx[keep], cs[keep])
+    assert sx[gone].isnan().all()
+    codes = xq.float()
+    assert not codes[:, K:].any()
+    if qt == 1:
+        assert codes[gone, :K].isnan().all()
+    else:
+        assert not codes[gone].any()
+    wq = (torch.arange(16 * xq.shape[1], device="cuda").reshape(16, -1) % 3).to(torch.int8)
+    wq = wq if qt == 0 else wq.float().to(torch.float8_e4m3fn)
+    one = torch.ones(1, device="cuda")
+    y = w8.w8a8_linear(xq, sx, wq, one, torch.zeros(16, dtype=torch.bfloat16, device="cuda"))
+    assert y[gone].isnan().all() and y[keep].isfinite().all()
+
+
+@pytest.mark.parametrize("qt", [0, 1])
+@pytest.mark.parametrize("K", [1001, 4096, 17000])
+def test_codes_of_an_infinite_or_nan_column(w8, qt, K):
+    """An infinite bias makes one column of y infinite: the scale is infinite,
+    a finite value over it is a zero of its sign, inf / inf is NaN (int8: 0).
+    A NaN in the weight makes every row's scale NaN."""
+    x, _, w, b = _inputs(5, K, "bf16", "f32", seed=K)
+    b[7] = float("-inf")
+    y, _, _ = w8.layer_norm_forward(x.cuda(), w.cuda(), b.cuda())
+    xq, sx = w8.w8a8_quant_act_rowwise_layer_norm(x.cuda(), w.cuda(), b.cuda(), qtype=qt)
+    assert torch.isposinf(sx).all()
+    codes, col = xq.float()[:, :K], torch.arange(K) != 7
+    assert not codes[:, col].any() and not xq.float()[:, K:].any()
+    if qt == 1:
+        assert codes[:, 7].isnan().all()
+        assert torch.equal(torch.signbit(codes[:, col]), torch.signbit(y[:, col]))
+    else:
+        assert not codes[:, 7].any()
+    b[7], w[9] = 0.0, float("nan")
+    xq, sx = w8.w8a8_quant_act_rowwise_layer_norm(x.cuda(), w.cuda(), b.cuda(), qtype=qt)
+    assert sx.isnan().all() and (qt == 0 or xq.float()[:, :K].isnan().all()) and not xq.float()[:, K:].any()

@@ -108,10 +108,13 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int d = 1; d < 16; d *= 2) v += dpp_shr(v, 0.f, d);
     return (lane_value(v, 15) + lane_value(v, 31)) + (lane_value(v, 47) + lane_value(v, 63));
 }
-__device__ __forceinline__ float wave_max(float v) {  // of values >= 0
+// The greater of two values, NaN if either is (fmaxf would drop it): one
+// instruction, as fmaxf is.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float wave_max(float v) {  // of values >= 0 or NaN
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) v = fmaxf(v, dpp_shr(v, 0.f, d));
-    return fmaxf(fmaxf(lane_value(v, 15), lane_value(v, 31)), fmaxf(lane_value(v, 47), lane_value(v, 63)));
+    for (int d = 1; d < 16; d *= 2) v = max_or_nan(v, dpp_shr(v, 0.f, d));
+    return max_or_nan(max_or_nan(lane_value(v, 15), lane_value(v, 31)), max_or_nan(lane_value(v, 47), lane_value(v, 63)));
 }
 
 // Sum over a workgroup of WAVES waves, the same value in every thread; `part`
@@ -135,7 +138,7 @@ __device__ __forceinline__ float group_max(float v, float *part) {
     __syncthreads();
     float s = part[0];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s = fmaxf(s, part[w]);
+    for (int w = 1; w < WAVES; ++w) s = max_or_nan(s, part[w]);
     return s;
 }
 

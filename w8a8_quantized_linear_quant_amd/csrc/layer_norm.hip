@@ -53,27 +53,38 @@ __global__ __launch_bounds__(kThreads) void ln_forward_kernel(const void *xv, in
     }
 }
 
-// Codes of 4 f32 values (one word, element order) with the shared rule;
-// r = f32(1 / s).
+// What the codes of a row are computed with.  A row that holds a NaN has a NaN
+// scale, from which every quotient is NaN.  An infinite scale s has x / s = 0
+// with x's sign, NaN for an infinite x: the quotient's correction would make
+// NaN of all (0 * inf); divisor 1 and reciprocal 0 give these values.  int8 has
+// no NaN: every code beside a scale that is not finite is 0.
+struct RowScale {
+    float s, r;      // divisor and its reciprocal
+    uint32_t keep;   // int8: the codes' bits that stay
+};
+__device__ __forceinline__ RowScale row_scale(float s) {
+    return {__builtin_isinf(s) ? 1.0f : s, 1.0f / s, __builtin_isfinite(s) ? ~0u : 0u};
+}
+
+// Codes of 4 f32 values (one word, element order) with the shared rule.
 template <int QT>
-__device__ __forceinline__ uint32_t codes4(const float *v, float s, float r) {
+__device__ __forceinline__ uint32_t codes4(const float *v, const RowScale &s) {
     if constexpr (QT == W8A8_INT8) {
         const float magic = 12582912.0f;  // 1.5 * 2^23: the add rounds half to even
         uint32_t b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(quotient_nosign(v[i], s, r) + magic);
-        return __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(quotient_nosign(v[i], s.s, s.r) + magic);
+        return (__builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu)) & s.keep;
     } else {
         // |v| <= absmax gives |v / s| <= 448 (1 + 2^-23), which converts to 448:
         // the clamp of the definition cannot bind
         float q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = quotient(v[i], s, r);
+        for (int i = 0; i < 4; ++i) q[i] = quotient(v[i], s.s, s.r);
         const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
     }
 }
-
 // ---------------------------------------------------------------- resident
 // Rows that fit the registers of one workgroup are read once: W waves share a
 // row, thread t of the row's 64 W holds its chunks t, t + 64 W, ... (16 bytes
@@ -257,11 +268,11 @@ __global__ __launch_bounds__(kResidentThreads<W>) void ln_resident_kernel(const 
                 float y = __builtin_fmaf((v[i][e] - mean) * rstd, param(wc[i], e), param(bc[i], e));
                 if constexpr (OUT != kOutNorm) {
                     if constexpr (!EVEN) y = col + e < K ? y : 0.f;
-                    most = fmaxf(most, fabsf(y));
+                    most = max_or_nan(most, fabsf(y));
                 }
                 v[i][e] = y;
             }
-            if constexpr (OUT != kOutNorm) top = fmaxf(top, col < K ? most : 0.f);
+            if constexpr (OUT != kOutNorm) top = max_or_nan(top, col < K ? most : 0.f);
             if constexpr (OUT == kOutNorm) {
                 E *y = static_cast<E *>(yv) + m * ldy;
                 if (m < M && col < K) {
@@ -281,11 +292,11 @@ __global__ __launch_bounds__(kResidentThreads<W>) void ln_resident_kernel(const 
                 if ((tid & 63) == 0) top_part[flip][group][tid >> 6] = top;
                 __syncthreads();
 #pragma unroll
-                for (int k = 0; k < W; ++k) top = fmaxf(top, top_part[flip][group][k]);
+                for (int k = 0; k < W; ++k) top = max_or_nan(top, top_part[flip][group][k]);
             }
             if (m >= M) continue;
             const float s = absmax_scale(top, QT == W8A8_INT8 ? 127.0f : 448.0f);
-            const float r = 1.0f / s;
+            const RowScale rs = row_scale(s);
             uint8_t *q = static_cast<uint8_t *>(yv) + m * ldy;
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
@@ -293,9 +304,14 @@ __global__ __launch_bounds__(kResidentThreads<W>) void ln_resident_kernel(const 
                 if (col >= ldy) continue;
                 uint32_t c[V / 4];
 #pragma unroll
-                for (int e = 0; e < V; e += 4) c[e / 4] = col < K ? codes4<QT>(&v[i][e], s, r) : 0u;
+                for (int e = 0; e < V; e += 4) c[e / 4] = col < K ? codes4<QT>(&v[i][e], rs) : 0u;
                 if constexpr (V == 8) *reinterpret_cast<uint2 *>(q + col) = make_uint2(c[0], c[1]);
                 else *reinterpret_cast<uint32_t *>(q + col) = c[0];
+            }
+            if constexpr (!EVEN && QT == W8A8_FP8_E4M3) {
+                // beside a NaN the chunk over K's end got NaN past K too: its own thread clears them
+                if (s != s && tid == K / V % T)
+                    for (int col = K; col % V != 0; ++col) q[col] = 0;
             }
             for (int64_t col = (int64_t)(NCH * T + tid) * V; col < ldy; col += T * V) {
                 if constexpr (V == 8) *reinterpret_cast<uint2 *>(q + col) = make_uint2(0u, 0u);
@@ -308,11 +324,11 @@ __global__ __launch_bounds__(kResidentThreads<W>) void ln_resident_kernel(const 
 
 // Code of one f32 value with the shared rule.
 template <int QT>
-__device__ __forceinline__ uint8_t code1(float v, float s, float r) {
+__device__ __forceinline__ uint8_t code1(float v, const RowScale &s) {
     if constexpr (QT == W8A8_INT8) {
-        return (uint8_t)(__float_as_uint(quotient_nosign(v, s, r) + 12582912.0f));  // 1.5 * 2^23: rounds half to even
+        return (uint8_t)(__float_as_uint(quotient_nosign(v, s.s, s.r) + 12582912.0f) & s.keep);  // as codes4
     } else {
-        const float q = __builtin_amdgcn_fmed3f(quotient(v, s, r), -448.0f, 448.0f);
+        const float q = quotient(v, s.s, s.r);
         return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false);
     }
 }
@@ -329,15 +345,15 @@ __global__ __launch_bounds__(kThreads) void ln_quant_kernel(const void *xv, int6
     float top = 0.f;
     for (int k = threadIdx.x; k < K; k += kThreads) {
         const float h = (X::load(x + k) - mean) * rstd;
-        top = fmaxf(top, fabsf(__builtin_fmaf(h, load_param(w, wt, k, 1.f), load_param(b, wt, k, 0.f))));
+        top = max_or_nan(top, fabsf(__builtin_fmaf(h, load_param(w, wt, k, 1.f), load_param(b, wt, k, 0.f))));
     }
     const float s = absmax_scale(group_max<kWaves>(top, part), QT == W8A8_INT8 ? 127.0f : 448.0f);
-    const float r = 1.0f / s;
+    const RowScale rs = row_scale(s);
     for (int64_t k = threadIdx.x; k < ldq; k += kThreads) {
         uint8_t c = 0;
         if (k < K) {
             const float h = (X::load(x + k) - mean) * rstd;
-            c = code1<QT>(__builtin_fmaf(h, load_param(w, wt, k, 1.f), load_param(b, wt, k, 0.f)), s, r);
+            c = code1<QT>(__builtin_fmaf(h, load_param(w, wt, k, 1.f), load_param(b, wt, k, 0.f)), rs);
         }
         xq[m * ldq + k] = c;
     }
