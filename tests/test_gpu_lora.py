@@ -381,3 +381,52 @@ def test_binding_refusals(w8):
         kw = dict(dict(dy=dy, x=x, u=u, **d), **b)
         with pytest.raises((TypeError, ValueError)):
             w8.lora_backward(**kw)
+
+
+# ------------------------------------------------------ infinite operands
+def _same(got, ref, bound, what):
+    """The infinities (with their signs) and NaN of the definition in 64 bits,
+    and its finite values within their bounds."""
+    got = got.cpu().to(f64)
+    for kind, f in (("NaN", torch.isnan), ("+inf", torch.isposinf), ("-inf", torch.isneginf)):
+        wrong = f(got) != f(ref)
+        assert not wrong.any(), f"{what}: {kind} differs at {int(wrong.sum())} of {wrong.numel()}: " \
+            f"got {got[wrong][0]}, ref {ref[wrong][0]}"
+    ok = ref.isfinite()
+    _near(got[ok], ref[ok], bound[ok], what)
+
+
+# few rows: one launch (R <= 16) or the ranks in parts; many columns or rows: 64 rows an up-projection workgroup
+INFINITE = [(40, 264, 328, 8), (40, 264, 328, 16), (70, 264, 328, 32), (70, 264, 328, 72), (8300, 2056, 72, 16),
+            (8300, 72, 2056, 64), (8300, 72, 2056, 128)]
+
+
+@pytest.mark.parametrize("case", INFINITE, ids=lambda c: "M%d-K%d-N%d-R%d" % c)
+def test_an_infinite_factor_gives_infinities(w8, case):
+    """A finite u (or g) against an infinite entry of b (or a): the signed
+    infinity of their product, NaN only where infinities of both signs (or
+    0 * inf) meet.  u of row 0 is exactly two values of bf16, its other half 0."""
+    M, K, N, R = case
+    print(f"[lora] infinite factors {case}", flush=True)
+    t = Batch([M - 9, 9], [1, 0], K, N, R, 2, seed=M + R)
+    t.x[0] = 0
+    t.x[0, 0] = 1.0                                              # u[0] = scale a[1, :, 0]
+    t.scale[1] = 1.0
+    d = t.dev(w8)
+    _, u = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **d)  # of finite factors
+    j, inf = R - 3, float("inf")
+    t.b[1, 5, 2], t.b[1, 6, j], t.b[0, N - 1, 1] = inf, -inf, inf
+    t.b[1, 9, 0], t.b[1, 9, j] = inf, inf                        # products of both signs in most rows
+    out, _ = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **t.dev(w8))
+    ref, _, eo, _ = t.forward()
+    assert torch.isinf(ref).any() and ref.isnan().any()
+    _same(out, ref, eo, "out")
+    t = Batch([M - 9, 9], [1, 0], K, N, R, 2, seed=M + R)
+    t.a[1, 2, 5], t.a[1, j, 6], t.a[0, 1, K - 1] = inf, -inf, inf
+    t.a[1, 0, 9], t.a[1, j, 9] = -inf, inf
+    dx, da, db = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=t.dbase.cuda(), **t.dev(w8))
+    rx, ra, rb, ex, ea, eb = t.backward(u.cpu())
+    assert torch.isinf(rx).any() and rx.isnan().any()
+    _same(dx, rx, ex, "dx")
+    _same(da, ra, ea, "da")
+    _same(db, rb, eb, "db")

@@ -254,6 +254,12 @@ __global__ __launch_bounds__(64 * down_waves(JB, RB)) void lora_down_kernel(cons
 // turns v into two bf16 halves (hi + lo, ~16 bits) in LDS; up to R = 16 both
 // fit one 32-wide contraction, the weight twice.
 constexpr int kUpWaves = 4;
+// Waves to a SIMD that the registers allow: 32 (RB = 2) or 64 of base, 32 for
+// each 32 ranks of the weight, 32 of sums.
+constexpr int up_simd_waves(int JB, int RB) {
+    if (JB <= 2) return RB == 2 ? 4 : 3;
+    return JB == 4 ? (RB == 2 ? 3 : 2) : 1;
+}
 
 // Four f32 values as bf16 halves; lo = 0 beside an infinite hi.
 __device__ __forceinline__ void split2(v4f f, uint2 &hi, uint2 &lo) {
@@ -336,13 +342,22 @@ __device__ __forceinline__ void up_fragments(v4u (&wf)[8][KB], int k, const v4u 
     }
 }
 
+// v's fragment of 16 rows for contraction k: from its hi or its lo half (JB = 1:
+// both in one contraction, the lanes of fg 2 and 3 hold lo).
+template <int JB, int P>
+__device__ __forceinline__ v4u v_fragment(const uint16_t (*hi)[P], const uint16_t (*lo)[P], int k, int h, int lane) {
+    const int fi = lane & 15, fg = lane >> 4, jg = JB == 1 ? fg & 1 : fg;
+    return *reinterpret_cast<const v4u *>(&((JB == 1 ? fg >> 1 : h) ? lo : hi)[fi][k * 32 + jg * 8]);
+}
+
 // One block of 16 rows of a wave's 128 columns: base (bf) plus v (its halves in
-// LDS rows hi, lo of this block) times the weight, stored.
+// LDS rows hi, lo of this block) times the weight, stored, unless a lane holds a
+// NaN in it: returns whether.  (Looking costs 16 instructions.)
 template <int JB, int KB, int P>
-__device__ __forceinline__ void up_rows(const v4u (&bf)[4], const uint16_t (*hi)[P], const uint16_t (*lo)[P],
+__device__ __forceinline__ bool up_rows(const v4u (&bf)[4], const uint16_t (*hi)[P], const uint16_t (*lo)[P],
                                         const v4u (&wf)[8][KB], int r, uint16_t *out, int64_t ldout, int rows, int col0,
                                         int C) {
-    const int lane = threadIdx.x & 63, fi = lane & 15, fg = lane >> 4, jg = JB == 1 ? fg & 1 : fg;
+    const int lane = threadIdx.x & 63, fg = lane >> 4;
     v4f acc[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
@@ -353,22 +368,82 @@ __device__ __forceinline__ void up_rows(const v4u (&bf)[4], const uint16_t (*hi)
         for (int k = 0; k < KB; ++k) {
 #pragma unroll
             for (int h = 0; h < (JB == 1 ? 1 : 2); ++h) {
-                const uint16_t(*v)[P] = (JB == 1 ? fg >> 1 : h) ? lo : hi;
-                const v4u f = *reinterpret_cast<const v4u *>(&v[fi][k * 32 + jg * 8]);
+                const v4u f = v_fragment<JB, P>(hi, lo, k, h, lane);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) acc[t] = mfma(f, wf[t][k], acc[t]);
             }
         }
     }
-    const int c = col0 + 8 * fi;
+    const int c = col0 + 8 * (lane & 15);
+    float any = 0.f;
+    v4u d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            any = max_or_nan(any, max_or_nan(acc[2 * p][e], acc[2 * p + 1][e]));
+            d[e][p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
+        }
+    if (__builtin_expect(__any(any != any && c < C), false)) return false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int row = 4 * fg + e;
-        if (row >= rows || c >= C) continue;
-        v4u d;
+        if (row < rows && c < C) *reinterpret_cast<v4u *>(out + row * ldout + c) = d[e];
+    }
+    return true;
+}
+
+// A pair of bf16 with its infinities and NaN as 0.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    return ((w & 0x7F80u) != 0x7F80u ? w & 0xFFFFu : 0u) | ((w & 0x7F800000u) != 0x7F800000u ? w & 0xFFFF0000u : 0u);
+}
+
+// The blocks (bits of `again`) that up_rows did not store.  Against an infinite
+// weight the two halves of v may give inf - inf or inf * 0 where v gives an
+// infinity: here lo meets the weight's finite entries alone, and the infinities
+// hi, which has v's sign.  base is still in place and read again.  Two columns
+// at a time, their results over their base, to need no more registers than up_rows.
+template <int JB, int KB, int P>
+__device__ __forceinline__ void up_again(unsigned again, __amdgpu_buffer_rsrc_t rb, int64_t ldbase,
+                                         const uint16_t (*hi)[P], const uint16_t (*lo)[P], const v4u (&wf)[8][KB],
+                                         uint16_t *out, int64_t ldout, int rows, int col0, int C) {
+    const int lane = threadIdx.x & 63, fg = lane >> 4, c = col0 + 8 * (lane & 15);
+#pragma unroll 1
+    for (; again != 0; again &= again - 1) {
+        const int first = __builtin_ctz(again) * 16;
+        v4u d[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) d[p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
-        *reinterpret_cast<v4u *>(out + row * ldout + c) = d;
+        for (int e = 0; e < 4; ++e) d[e] = load16(rb, (int)((first + 4 * fg + e) * ldbase + c) * 2);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            v4f acc[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[0][e] = __uint_as_float(d[e][p] << 16), acc[1][e] = __uint_as_float(d[e][p] & 0xFFFF0000u);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int h = 0; h < (JB == 1 ? 1 : 2); ++h) {
+                    const v4u f = v_fragment<JB, P>(hi + first, lo + first, k, h, lane);
+                    const bool is_lo = JB == 1 ? fg >> 1 : h;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v4u w = wf[2 * p + i][k];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            asm volatile("" : "+v"(w[q]));  // or all of them are made, and held, ahead of the loop
+                            w[q] = is_lo ? finite_halves(w[q]) : w[q];
+                        }
+                        acc[i] = mfma(f, w, acc[i]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e][p] = pack_bf16x2(acc[0][e], acc[1][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (4 * fg + e < rows - first && c < C) *reinterpret_cast<v4u *>(out + (first + 4 * fg + e) * ldout + c) = d[e];
     }
 }
 
@@ -403,7 +478,7 @@ __device__ __forceinline__ void add_splits(const SplitSums &sums, int block) {
 }
 
 template <int JB, bool TR, int RB>
-__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
+__global__ __launch_bounds__(64 * kUpWaves, up_simd_waves(JB, RB)) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
                                                                 int L, int R, const int32_t *ranks,
                                                                 const int32_t *plan, int groups, const uint16_t *base,
                                                                 int64_t ldbase, uint16_t *out, int64_t ldout,
@@ -462,12 +537,15 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(const float *v, 
     }
     __syncthreads();
     if (col0 >= C) return;
+    unsigned again = 0;
 #pragma unroll
     for (int a = 0; a < RB; ++a) {
         if (a * 16 >= tile.rows) break;
-        up_rows<JB, KB, P>(bf[a], &vs[0][a * 16], &vs[1][a * 16], wf, r, out + (tile.row0 + a * 16) * ldout, ldout,
-                           tile.rows - a * 16, col0, C);
+        if (!up_rows<JB, KB, P>(bf[a], &vs[0][a * 16], &vs[1][a * 16], wf, r, out + (tile.row0 + a * 16) * ldout,
+                                       ldout, tile.rows - a * 16, col0, C))
+            again |= 1u << a;
     }
+    up_again<JB, KB, P>(again, rb, ldbase, vs[0], vs[1], wf, out + tile.row0 * ldout, ldout, tile.rows, col0, C);
 }
 
 // ---------------------------------------------------------------- both
@@ -528,7 +606,8 @@ __global__ __launch_bounds__(1024) void lora_both_kernel(const uint16_t *x, int6
     __syncthreads();
     if (col0 >= C2) return;
     up_fragments<JB, TR>(wf, 0, d, lds + wave * kArea, R, r);
-    up_rows<JB, KB, P>(bf, vs[0], vs[1], wf, r, out + row0 * ldout, ldout, rows, col0, C2);
+    const bool stored = up_rows<JB, KB, P>(bf, vs[0], vs[1], wf, r, out + row0 * ldout, ldout, rows, col0, C2);
+    up_again<JB, KB, P>(stored ? 0u : 1u, rb, ldbase, vs[0], vs[1], wf, out + row0 * ldout, ldout, rows, col0, C2);
 }
 
 // --------------------------------------------------------------- outer sums
