@@ -430,3 +430,20 @@ def test_an_infinite_factor_gives_infinities(w8, case):
     _same(dx, rx, ex, "dx")
     _same(da, ra, ea, "da")
     _same(db, rb, eb, "db")
+
+
+def test_a_u_near_the_largest_number(w8):
+    """u is finite but nearest to no finite bf16: its products are finite."""
+    t = Batch([3], [0], 64, 64, 8, 1, seed=6)
+    t.x.zero_()
+    t.a.zero_()
+    t.x[1, 0], t.a[0, 0, 0] = torch.finfo(torch.bfloat16).max, 1.0
+    t.scale = torch.tensor([1.003])
+    t.b.zero_()
+    t.b[0, :32, 0], t.b[0, 40, 0] = 2.0 ** -20, -2.0 ** -20
+    t.base.zero_()
+    out, u = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **t.dev(w8))
+    ref, refu, eo, eu = t.forward()
+    assert refu[1, 0] > 3.3962e38 and u.isfinite().all()
+    _same(u, refu, eu, "u")
+    _same(out, ref, eo, "out")

@@ -261,12 +261,17 @@ constexpr int up_simd_waves(int JB, int RB) {
     return JB == 4 ? (RB == 2 ? 3 : 2) : 1;
 }
 
-// Four f32 values as bf16 halves; lo = 0 beside an infinite hi.
+// Four f32 values as bf16 halves; lo = 0 beside an infinite hi.  A finite value
+// nearest to no finite bf16 takes the largest one for its hi.
+__device__ __forceinline__ float split_hi(float f) {
+    constexpr float most = 0x1.FEp127f;
+    return __builtin_isfinite(f) ? __builtin_amdgcn_fmed3f(f, -most, most) : f;
+}
 __device__ __forceinline__ void split2(v4f f, uint2 &hi, uint2 &lo) {
     uint32_t h[2], l[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-        h[p] = pack_bf16x2(f[2 * p], f[2 * p + 1]);
+        h[p] = pack_bf16x2(split_hi(f[2 * p]), split_hi(f[2 * p + 1]));
         const float a = __uint_as_float(h[p] << 16), b = __uint_as_float(h[p] & 0xFFFF0000u);
         l[p] = pack_bf16x2(__builtin_isfinite(a) ? f[2 * p] - a : 0.f, __builtin_isfinite(b) ? f[2 * p + 1] - b : 0.f);
     }
@@ -598,7 +603,7 @@ __global__ __launch_bounds__(1024) void lora_both_kernel(const uint16_t *x, int6
             for (int k = 0; k < W; ++k) t += part[k][row][threadIdx.x % 16];
             t = j < r ? t * s : 0.f;
             if (v && group == 0 && row < rows && j < R) v[(row0 + row) * R + j] = t;
-            const float hi = __uint_as_float(pack_bf16x2(t, 0.f) << 16);
+            const float hi = __uint_as_float(pack_bf16x2(split_hi(t), 0.f) << 16);
             vs[0][row][j] = (uint16_t)(__float_as_uint(hi) >> 16);
             vs[1][row][j] = (uint16_t)pack_bf16x2(__builtin_isfinite(hi) ? t - hi : 0.f, 0.f);
         }
