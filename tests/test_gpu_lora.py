@@ -447,3 +447,26 @@ def test_a_u_near_the_largest_number(w8):
     assert refu[1, 0] > 3.3962e38 and u.isfinite().all()
     _same(u, refu, eu, "u")
     _same(out, ref, eo, "out")
+
+
+@pytest.mark.parametrize("R", [8, 32, 64, 128])
+@pytest.mark.parametrize("lengths", [[70, 5], [700, 9]])
+def test_infinite_rows_in_the_gradients(w8, lengths, R):
+    """An infinity in dy or x against finite u and g: the signed infinity of
+    their product in dB's and dA's entries, NaN only where the definition has
+    it."""
+    print(f"[lora] infinite rows {lengths} R{R}", flush=True)
+    t = Batch(lengths, [1, 0], 136, 264, R, 2, seed=R)
+    _, u = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **t.dev(w8))
+    u = u.cpu()
+    u[3] = u[3].bfloat16().float()                               # exactly bf16: its other parts are 0
+    u[3, 1] = 1.0
+    t.dy[3, 7], t.dy[30, 100], t.dy[31, 8] = float("inf"), float("-inf"), float("inf")
+    t.dy[32, 8] = float("-inf")                                  # both signs in column 8: inf or NaN by u's signs
+    t.x[5, 9], t.x[50, 135], t.x[lengths[0] + 1, 0] = float("inf"), float("-inf"), float("inf")
+    dx, da, db = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u.cuda(), base=t.dbase.cuda(), **t.dev(w8))
+    rx, ra, rb, ex, ea, eb = t.backward(u)
+    assert torch.isinf(ra).any() and torch.isinf(rb).any() and rb.isnan().any()
+    _same(db, rb, eb, "db")
+    _same(da, ra, ea, "da")
+    _same(dx, rx, ex, "dx")

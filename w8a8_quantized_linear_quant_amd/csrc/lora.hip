@@ -672,25 +672,15 @@ __device__ __forceinline__ v4u read_transposed(const char *area, int m0, int pie
     return v4u{a.x, a.y, b.x, b.y};
 }
 
-// Block q of dA's or dB's: by adapter, split, columns.
-template <int JB, bool RANKS_FIRST>
-__device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, int L, int R, const int32_t *ranks,
-                                            const int32_t *plan, int T, int splits, char *ys,
-                                            char (&vs)[3][kTileRows * 32 * JB]) {
+// acc = the sums of tiles begin .. end - 1: a wave's NC x NJ blocks of 16 x 16 of
+// the 128 x 16 JB output, from pieces pc and pj.  FINITE: v's second and third
+// parts meet the finite entries of y alone.
+template <int JB, bool RANKS_FIRST, bool FINITE, int NC, int NJ>
+__device__ __forceinline__ void outer_sums(v4f (&acc)[NC][NJ], const Outer &o, int col0, int pc, int pj, int64_t M, int L,
+                                           int R, const int32_t *plan, int begin, int end, char *ys,
+                                           char (&vs)[3][kTileRows * 32 * JB]) {
     constexpr int kThreads = 64 * kOuterWaves;
-    // a wave's part of the 128 x 16 JB output: NC x NJ blocks of 16 x 16
-    constexpr int NC = JB == 1 ? 2 : 4, NJ = JB == 1 ? 1 : JB / 2;
-    const int col0 = q % o.groups * 128;
-    q /= o.groups;
-    const int split = q % splits, l = q / splits;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int pc = JB == 1 ? wave * 2 : (wave & 1) * 4, pj = JB == 1 ? 0 : (wave >> 1) * NJ;  // its first pieces
-    const int r = rank_of(ranks, l, R);
-    const int32_t *first = plan + 4 * (int64_t)T;
-    const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
-    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits);
-    const int end = t0 + (int)((int64_t)n * (split + 1) / splits);
-    v4f acc[NC][NJ];
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -722,46 +712,119 @@ __device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, in
             }
             __builtin_amdgcn_sched_barrier(0);
         };
-        fetch(0, yd[0], vd[0]);
-        fetch(1, yd[1], vd[1]);
-        for (int i = 0; i < count; i += 2) {
+        auto stage_y = [&](const v4u (&y)[4]) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                // (an odd count's last turn adds the 0 of a tile past the end)
-                __syncthreads();  // the last tile's fragments have been read
+            for (int k = 0; k < 4; ++k) {
+                const int row = k * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+                *reinterpret_cast<v4u *>(ys + piece_at<8>(row, c >> 1) + (c & 1) * 16) = y[k];
+            }
+        };
+        auto stage_v = [&](const v4u (&v)[JB]) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = k * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
-                    *reinterpret_cast<v4u *>(ys + piece_at<8>(row, c >> 1) + (c & 1) * 16) = yd[p][k];
-                }
+            for (int k = 0; k < JB; ++k) {
+                const int q = k * kThreads + threadIdx.x, row = q / (4 * JB), j = q % (4 * JB) * 4;
+                uint2 s[3];
+                split3(__builtin_bit_cast(v4f, v[k]), s);
 #pragma unroll
-                for (int k = 0; k < JB; ++k) {
-                    const int q = k * kThreads + threadIdx.x, row = q / (4 * JB), j = q % (4 * JB) * 4;
-                    uint2 s[3];
-                    split3(__builtin_bit_cast(v4f, vd[p][k]), s);
+                for (int h = 0; h < 3; ++h)
+                    *reinterpret_cast<uint2 *>(vs[h] + piece_at<JB>(row, j >> 4) + (j & 15) * 2) = s[h];
+            }
+        };
+        // y times v's parts FROM .. TO - 1
+        auto multiply = [&]<int FROM, int TO>() {
 #pragma unroll
-                    for (int h = 0; h < 3; ++h)
-                        *reinterpret_cast<uint2 *>(vs[h] + piece_at<JB>(row, j >> 4) + (j & 15) * 2) = s[h];
-                }
-                fetch(i + p + 2, yd[p], vd[p]);
+            for (int m0 = 0; m0 < kTileRows; m0 += 32) {
+                v4u yf[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) yf[c] = read_transposed<8>(ys, m0, pc + c, lane);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int h = FROM; h < TO; ++h) {
+                        const v4u f = read_transposed<JB>(vs[h], m0, pj + j, lane);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            acc[c][j] = RANKS_FIRST ? mfma(f, yf[c], acc[c][j]) : mfma(yf[c], f, acc[c][j]);
+                    }
+            }
+        };
+        if constexpr (FINITE) {  // seldom run: one tile in flight, for fewer registers
+            for (int i = 0; i < count; ++i) {
+                fetch(i, yd[0], vd[0]);
+                __syncthreads();
+                stage_y(yd[0]);
+                stage_v(vd[0]);
+                __syncthreads();
+                multiply.template operator()<0, 1>();
                 __syncthreads();
 #pragma unroll
-                for (int m0 = 0; m0 < kTileRows; m0 += 32) {
-                    v4u yf[NC];
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) yf[c] = read_transposed<8>(ys, m0, pc + c, lane);
+                    for (int p = 0; p < 4; ++p) yd[0][k][p] = finite_halves(yd[0][k][p]);
+                stage_y(yd[0]);
+                __syncthreads();
+                multiply.template operator()<1, 3>();
+            }
+        } else {
+            fetch(0, yd[0], vd[0]);
+            fetch(1, yd[1], vd[1]);
+            for (int i = 0; i < count; i += 2) {
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                        for (int h = 0; h < 3; ++h) {
-                            const v4u f = read_transposed<JB>(vs[h], m0, pj + j, lane);
-#pragma unroll
-                            for (int c = 0; c < NC; ++c)
-                                acc[c][j] = RANKS_FIRST ? mfma(f, yf[c], acc[c][j]) : mfma(yf[c], f, acc[c][j]);
-                        }
+                for (int p = 0; p < 2; ++p) {
+                    // (an odd count's last turn adds the 0 of a tile past the end)
+                    __syncthreads();  // the last tile's fragments have been read
+                    stage_y(yd[p]);
+                    stage_v(vd[p]);
+                    fetch(i + p + 2, yd[p], vd[p]);
+                    __syncthreads();
+                    multiply.template operator()<0, 3>();
                 }
             }
         }
+    }
+}
+
+// Block q of dA's or dB's: by adapter, split, columns.
+template <int JB, bool RANKS_FIRST>
+__device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, int L, int R, const int32_t *ranks,
+                                            const int32_t *plan, int T, int splits, char *ys,
+                                            char (&vs)[3][kTileRows * 32 * JB]) {
+    constexpr int NC = JB == 1 ? 2 : 4, NJ = JB == 1 ? 1 : JB / 2;
+    const int col0 = q % o.groups * 128;
+    q /= o.groups;
+    const int split = q % splits, l = q / splits;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int pc = JB == 1 ? wave * 2 : (wave & 1) * 4, pj = JB == 1 ? 0 : (wave >> 1) * NJ;  // its first pieces
+    const int r = rank_of(ranks, l, R);
+    const int32_t *first = plan + 4 * (int64_t)T;
+    const int t0 = T ? min(max(first[l], 0), T) : 0, t1 = T ? min(max(first[l + 1], t0), T) : 0;
+    const int n = t1 - t0, begin = t0 + (int)((int64_t)n * split / splits);
+    const int end = t0 + (int)((int64_t)n * (split + 1) / splits);
+    v4f acc[NC][NJ];
+    outer_sums<JB, RANKS_FIRST, false>(acc, o, col0, pc, pj, M, L, R, plan, begin, end, ys, vs);
+    // Against an infinity of y the parts of v may give inf - inf or inf * 0 where v
+    // gives an infinity: with a NaN among the results the block's sums are taken
+    // again, the infinities meeting v's first part alone, which has v's sign.
+    const int across = 4 * (lane >> 4), along = lane & 15;
+    float any = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int b = 0; b < NJ; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = col0 + (pc + c) * 16 + (RANKS_FIRST ? along : across + e);
+                const int j = (pj + b) * 16 + (RANKS_FIRST ? across + e : along);
+                any = max_or_nan(any, col < o.C && j < r ? acc[c][b][e] : 0.f);
+            }
+    __syncthreads();  // every wave has read the last tile
+    if (lane == 0) reinterpret_cast<int *>(ys)[wave] = 0;
+    if (any != any) reinterpret_cast<int *>(ys)[wave] = 1;
+    __syncthreads();
+    const v4i flags = *reinterpret_cast<const v4i *>(ys);
+    if (__builtin_expect((flags[0] | flags[1] | flags[2] | flags[3]) != 0, false)) {
+        __syncthreads();
+        outer_sums<JB, RANKS_FIRST, true>(acc, o, col0, pc, pj, M, L, R, plan, begin, end, ys, vs);
     }
     // the contiguous index of d along 16 lanes: rows of the product are ranks
     // (dA) or columns (dB)
@@ -772,18 +835,19 @@ __device__ __forceinline__ void outer_block(const Outer &o, int q, int64_t M, in
         for (int b = 0; b < NJ; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int across = 4 * (lane >> 4) + e, along = lane & 15;
-                const int col = col0 + (pc + c) * 16 + (RANKS_FIRST ? along : across);
-                const int j = (pj + b) * 16 + (RANKS_FIRST ? across : along);
+                const int col = col0 + (pc + c) * 16 + (RANKS_FIRST ? along : across + e);
+                const int j = (pj + b) * 16 + (RANKS_FIRST ? across + e : along);
                 if (col < o.C && j < R)
                     d[RANKS_FIRST ? (int64_t)j * o.C + col : (int64_t)col * R + j] = j < r ? acc[c][b][e] : 0.f;
             }
 }
 
+// Waves to a SIMD that the registers allow, with two tiles in flight.
+constexpr int outer_simd_waves(int JB) { return JB == 1 ? 5 : JB == 2 ? 3 : 2; }
+
 template <int JB>
-__global__ __launch_bounds__(64 * kOuterWaves) void lora_outer_kernel(OuterPair both, int64_t M, int L, int R,
-                                                                      const int32_t *ranks, const int32_t *plan, int T,
-                                                                      int splits) {
+__global__ __launch_bounds__(64 * kOuterWaves, outer_simd_waves(JB)) void lora_outer_kernel(
+    OuterPair both, int64_t M, int L, int R, const int32_t *ranks, const int32_t *plan, int T, int splits) {
     __shared__ __attribute__((aligned(16))) char ys[kTileRows * 256], vs[3][kTileRows * 32 * JB];
     const int na = both.a.groups * L * splits, q = blockIdx.x;
     if (q < na) outer_block<JB, true>(both.a, q, M, L, R, ranks, plan, T, splits, ys, vs);
