@@ -470,3 +470,20 @@ def test_infinite_rows_in_the_gradients(w8, lengths, R):
     _same(db, rb, eb, "db")
     _same(da, ra, ea, "da")
     _same(dx, rx, ex, "dx")
+
+
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7F800001, -0x7FFFFF])
+@pytest.mark.parametrize("R", [8, 128])
+def test_any_nan_of_u_is_a_nan_of_db(w8, bits, R):
+    """Whatever the NaN's payload and sign (the cut to bf16 parts must not
+    leave an infinity of one whose payload is in its low bits)."""
+    t = Batch([70, 5], [1, 0], 136, 264, R, 2, seed=R)
+    _, u = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **t.dev(w8))
+    u = u.cpu()
+    u[12, R - 1] = torch.tensor(bits, dtype=torch.int32).view(torch.float32)
+    assert u[12, R - 1].isnan()
+    _, da, db = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u.cuda(), base=t.dbase.cuda(), **t.dev(w8))
+    _, ra, rb, _, ea, eb = t.backward(u)
+    _same(db, rb, eb, "db")
+    _same(da, ra, ea, "da")
+    assert db[1, :, R - 1].isnan().all()

@@ -637,7 +637,8 @@ struct OuterPair {
 };
 
 // Four f32 values as three bf16 parts: the first two are cut (not rounded) off
-// the remainder, so each remainder is exact; an infinity or NaN has none.
+// the remainder, so each remainder is exact; an infinity has none, a NaN's is NaN
+// (the first part alone may be an infinity, where the payload is in the low bits).
 __device__ __forceinline__ void split3(v4f f, uint2 (&s)[3]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -647,7 +648,7 @@ __device__ __forceinline__ void split3(v4f f, uint2 (&s)[3]) {
         s[i] = make_uint2(h[0], h[1]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            f[k] = i || __builtin_isfinite(f[k]) ? f[k] - __uint_as_float(__float_as_uint(f[k]) & 0xFFFF0000u) : 0.f;
+            f[k] = i || !__builtin_isinf(f[k]) ? f[k] - __uint_as_float(__float_as_uint(f[k]) & 0xFFFF0000u) : 0.f;
     }
     s[2] = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
 }
