@@ -431,3 +431,21 @@ def test_codes_of_an_infinite_or_nan_column(w8, qt, K):
     b[7], w[9] = 0.0, float("nan")
     xq, sx = w8.w8a8_quant_act_rowwise_layer_norm(x.cuda(), w.cuda(), b.cuda(), qtype=qt)
     assert sx.isnan().all() and (qt == 0 or xq.float()[:, :K].isnan().all()) and not xq.float()[:, K:].any()
+
+
+@pytest.mark.parametrize("K", [100, 101, 600])
+def test_backward_of_constant_rows_of_huge_values(w8, K):
+    """x - mean is 0 in every column that there is, so h is 0 and dx is
+    rstd (t - <t>), however large the mean; columns past K count for nothing."""
+    x, dy, w, _ = _inputs(4, K, "f32", "f32", seed=K)
+    x[1] = 2.0 ** (127 - int(np.ceil(np.log2(K))))               # the row's sum is finite, mean / sqrt(eps) is not
+    x[2] = -x[1]
+    y, mu, rs = w8.layer_norm_forward(x.cuda(), w.cuda(), eps=1e-7)
+    assert torch.equal(mu[1:3].cpu(), x[1:3, 0]) and not y[1:3].any()
+    for params in (True, False):
+        dx, dw, db = w8.layer_norm_backward(dy.cuda(), x.cuda(), mu, rs, w.cuda(), need_params=params)
+        rx, rw, rb, ex, ew, eb = _grad_reference(dy, x, mu.cpu(), rs.cpu(), w)
+        t = (dy * w).to(f64)
+        rx[1:3] = (rs.cpu().to(f64)[:, None] * (t - t.mean(1, keepdim=True)))[1:3]
+        ex[1:3] = (rs.cpu().to(f64)[:, None] * (K + 8) * E * (t.abs() + t.abs().mean(1, keepdim=True)))[1:3]
+        _near(dx, rx, ex, "dx")

@@ -418,10 +418,14 @@ __global__ __launch_bounds__(backward_threads(NCH * X::kVec)) void ln_backward_k
         for (int i = 0; i < NCH; ++i) {
             X::unpack(rx[i], h[i]);
             X::unpack(ry[i], t[i]);
-            // columns past K hold x = dy = 0: t = 0 there, whatever h
+            // columns past K hold x = dy = 0: t = 0 there, and h must be finite,
+            // which -mean rstd need not be
+            const int col = (i * T + tid) * V;
+            const float mean_i = EVEN && col >= K ? 0.f : mu, rstd_i = EVEN && col >= K ? 0.f : rs;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                h[i][e] = (h[i][e] - mu) * rs;
+                h[i][e] = (h[i][e] - mean_i) * rstd_i;
+                if constexpr (!EVEN) h[i][e] = col + e < K ? h[i][e] : 0.f;
                 if constexpr (PARAMS) {
                     aw[i][e] = __builtin_fmaf(t[i][e], h[i][e], aw[i][e]);
                     ab[i][e] += t[i][e];
