@@ -449,3 +449,26 @@ def test_backward_of_constant_rows_of_huge_values(w8, K):
         rx[1:3] = (rs.cpu().to(f64)[:, None] * (t - t.mean(1, keepdim=True)))[1:3]
         ex[1:3] = (rs.cpu().to(f64)[:, None] * (K + 8) * E * (t.abs() + t.abs().mean(1, keepdim=True)))[1:3]
         _near(dx, rx, ex, "dx")
+
+
+def test_dx_alone_of_very_many_rows(w8):
+    """2^26 rows and a few: more than one launch may have threads for with a
+    row each."""
+    M, K = 2 ** 26 + 3, 8
+    print(f"[norm] dx alone M{M}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    y, mu, rs = w8.layer_norm_forward(x)
+    dx, _, _ = w8.layer_norm_backward(dy, x, mu, rs)
+    for first in (0, 2 ** 22 - 50, 2 ** 24 - 50, 2 ** 25 + 7, M - 100):
+        rows = slice(first, first + 100)
+        rx, _, _, ex, _, _ = _grad_reference(dy[rows].cpu(), x[rows].cpu(), mu[rows].cpu(), rs[rows].cpu(), None)
+        _near(dx[rows], rx, ex + ROUND[torch.bfloat16] * (rx.abs() + ex), f"rows from {first}")
+        ry, rmu, rrs, ey, em, er, _, _ = _reference(x[rows].cpu(), None, None, 1e-5)
+        _near(y[rows], ry, ey + ROUND[torch.bfloat16] * (ry.abs() + ey), f"y from {first}")
+    again = torch.empty_like(dx)
+    for i in range(0, M, 2 ** 24):                                 # the same rows in smaller calls: the same bits
+        rows = slice(i, min(i + 2 ** 24, M))
+        w8.layer_norm_backward(dy[rows], x[rows], mu[rows], rs[rows], out=again[rows])
+    assert torch.equal(again, dx)

@@ -17,6 +17,10 @@ constexpr int kWaves = kThreads / 64;
 constexpr int64_t kMaxK = 1 << 24;
 constexpr int kMaxGroups = 256;      // workgroups of the backward kernel: one for each CU
 constexpr int kStreamSplits = 64;    // row splits of the streaming column sums
+// Workgroups of a launch at most: with their threads below HIP's 2^32.  More
+// rows than these have are taken by them in turn.  (Streamed rows are more than
+// 16384 wide: 2^24 of them, a workgroup each, fit no memory.)
+constexpr int64_t kMaxGrid = 1 << 22;
 
 // One workgroup per row, the row read again for each pass.
 template <class X>
@@ -683,7 +687,8 @@ void backward_dx_launch(const BackwardArgs &a, hipStream_t stream) {
 #define W8A8_LN(W_, E_)                                                                                     \
     if (lay.W == W_ && lay.ept == E_) {                                                                     \
         constexpr int groups = W_ < 4 ? 4 / W_ : 1;                                                         \
-        return backward_resident<X, W_, E_, false>(a, (int)((a.M + groups - 1) / groups), groups, stream);  \
+        const int64_t n = (a.M + groups - 1) / groups;                                                      \
+        return backward_resident<X, W_, E_, false>(a, (int)(n < kMaxGrid ? n : kMaxGrid), groups, stream);  \
     }
     W8A8_LN(1, 8) W8A8_LN(1, 16) W8A8_LN(2, 16) W8A8_LN(4, 16) W8A8_LN(8, 16) W8A8_LN(8, 32)
 #undef W8A8_LN
