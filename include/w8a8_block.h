@@ -51,8 +51,8 @@ typedef enum {
  * allowed), adapters [S] (-1 .. L - 1).  Writes the tile count T to *tiles
  * and, if plan is not NULL, the 4 T + L + 1 integers to plan (capacity
  * integers long, else W8A8_ERR_SHAPE).  Call it with plan = NULL for the
- * size.  The sum of the lengths is at most 2^30, L is in [1, 65535]
- * (W8A8_ERR_SHAPE); a negative length or an adapter outside the pool is
+ * size.  The sum of the lengths is at most 2^30, T at most 2^24, L is in
+ * [1, 65535] (W8A8_ERR_SHAPE); a negative length or an adapter outside the pool is
  * W8A8_ERR_INVALID_ARG.  All pointers are host pointers.
  */
 w8a8_status lora_plan(const int64_t *lengths, const int32_t *adapters, int64_t S, int64_t L, int32_t *plan,
@@ -72,8 +72,8 @@ w8a8_status lora_plan(const int64_t *lengths, const int32_t *adapters, int64_t S
  *   (in place, same stride).  u f32 [M, R] or NULL: what lora_backward takes.
  *   workspace lora_forward_workspace_bytes(M, R) bytes, used if u is NULL.
  * Rows in no tile are not written.
- * Shape rules: M >= 0, T >= 0, 1 <= L <= 65535; K, N, R, strides multiples of
- * 8; 8 <= R <= 128 (else W8A8_ERR_INVALID_ARG), 8 <= K, N <= 2^22,
+ * Shape rules: M >= 0, 0 <= T <= 2^24, 1 <= L <= 65535; K, N, R, strides
+ * multiples of 8; 8 <= R <= 128 (else W8A8_ERR_INVALID_ARG), 8 <= K, N <= 2^22,
  * M <= 2^30, strides from their width up to 2^22.
  */
 size_t lora_forward_workspace_bytes(int64_t M, int64_t R);

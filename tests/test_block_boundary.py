@@ -169,3 +169,8 @@ def test_binding_refuses_cpu_tensors():
         w8.layer_norm_backward(x, x, x, x)
     with pytest.raises(ValueError):
         w8.w8a8_quant_act_rowwise_layer_norm(x)
+
+
+@pytest.mark.parametrize("f", [_forward, _backward])
+def test_lora_refuses_more_tiles_than_a_plan_has(f):
+    assert f(M=1 << 30, T=(1 << 24) + 1) == SHAPE

@@ -487,3 +487,82 @@ def test_any_nan_of_u_is_a_nan_of_db(w8, bits, R):
     _same(db, rb, eb, "db")
     _same(da, ra, ea, "da")
     assert db[1, :, R - 1].isnan().all()
+
+
+# ------------------------------------------------- more than one launch holds
+def _rows_check(rows, l, s, x, u, out, base, a, b, what):
+    """u and out of some rows of adapter l against the definition."""
+    xf, af, bf, uf = x[rows].cpu().to(f64), a[l].cpu().to(f64), b[l].cpu().to(f64), u[rows].cpu().to(f64)
+    ru = s * (xf @ af.T)
+    eu = (xf.shape[1] + 8) * U23 * s * (xf.abs() @ af.abs().T)
+    _near(u[rows], ru, eu, what + " u")
+    basef = base[rows].cpu().to(f64)
+    ro = basef + uf @ bf.T
+    eo = (uf.abs() * (2.0 ** -16 + (2 * uf.shape[1] + 8) * U23)) @ bf.abs().T
+    _near(out[rows], ro, eo + 2.0 ** -8 * ro.abs() + 4 * U23 * basef.abs(), what + " out")
+
+
+@pytest.mark.parametrize("T,K,N", [(2 ** 22 + 3, 8, 8), (360001, 8, 1032), (360001, 1032, 8)])
+def test_requests_beyond_one_launch(w8, T, K, N):
+    """So many requests of one row that the workgroups' threads pass 2^32, or
+    the columns' workgroups a launch's most; every third without an adapter,
+    which comes first in the plan."""
+    print(f"[lora] {T} requests K{K} N{N}", flush=True)
+    R, L = 8, 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *shape: torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x, dy, base, dbase, a, b = rnd(T, K), rnd(T, N), rnd(T, N), rnd(T, K), rnd(L, R, K), rnd(L, N, R)
+    scale = torch.tensor([1.0, 0.5], device="cuda")
+    adapters = ([0, 1, -1] * (T // 3 + 1))[:T]
+    plan = w8.lora_plan([1] * T, adapters, L)
+    assert plan.tiles == T
+    out, u = w8.lora_forward(x, a, b, plan, scale=scale, base=base)
+    dx, da, db = w8.lora_backward(dy, x, u, a, b, plan, scale=scale, base=dbase)
+    v = torch.empty_like(u)                                      # g of the definition, rounded to f32
+    for l in range(L):
+        s = float(scale[l])
+        v[l::3] = (s * torch.mm(dy[l::3].to(f64), b[l].to(f64))).float()
+        picked = torch.tensor([l, l + 3 * (T // 9), l + 3 * (T // 6), l + 3 * ((T - 1 - l) // 3)])
+        _rows_check(picked, l, s, x, u, out, base, a, b, f"adapter {l}")
+        vr = v[picked].cpu().to(f64)
+        rx = dbase[picked].cpu().to(f64) + vr @ a[l].cpu().to(f64)
+        eg = (N + 8) * U23 * s * (dy[picked].cpu().to(f64).abs() @ b[l].cpu().to(f64).abs())
+        ex = (vr.abs() * (2.0 ** -16 + (2 * R + 8) * U23) + eg) @ a[l].cpu().to(f64).abs()
+        _near(dx[picked], rx, ex + 2.0 ** -8 * rx.abs() + 4 * U23 * dbase[picked].cpu().to(f64).abs(), "dx")
+        vl, xl, ul, dl = (t[l::3].to(f64) for t in (v, x, u, dy))
+        e = (vl.shape[0] + 16) * U23
+        egl = (N + 8) * U23 * s * torch.mm(dl.abs(), b[l].to(f64).abs())
+        _near(da[l], torch.mm(vl.t(), xl).cpu(), torch.mm((e * vl.abs() + egl).t(), xl.abs()).cpu(), "da")
+        _near(db[l], torch.mm(dl.t(), ul).cpu(), (e * torch.mm(dl.abs().t(), ul.abs())).cpu(), "db")
+    assert not u[2::3].any() and torch.equal(out[2::3], base[2::3]) and torch.equal(dx[2::3], dbase[2::3])
+    # every row: the same rows a part of the batch at a time give what the whole gave, but for the sums' order
+    for first in range(0, T, 3 * 2 ** 17):
+        rows = slice(first, min(first + 3 * 2 ** 17, T))
+        n = rows.stop - first
+        po, pu = w8.lora_forward(x[rows], a, b, w8.lora_plan([1] * n, adapters[rows], L), scale=scale, base=base[rows])
+        off = (po.float() - out[rows].float()).abs()
+        assert bool((off <= 2.0 ** -7 * po.float().abs() + 1e-3).all()), first
+        assert torch.allclose(pu, u[rows], rtol=1e-4, atol=1e-4), first
+
+
+def test_a_pool_beyond_one_launch(w8):
+    """The weights' gradients of 65535 adapters: more workgroups than a launch
+    has; a few of the adapters are used."""
+    print("[lora] 65535 adapters", flush=True)
+    L, K, N, R = 65535, 8, 2056, 8
+    used = [0, 777, 58254, 65534]
+    small = Batch([70, 1, 9, 130, 3], [2, 0, 3, 1, -1], K, N, R, 4, scale=False, seed=11)
+    a = torch.zeros((L, R, K), dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros((L, N, R), dtype=torch.bfloat16, device="cuda")
+    a[used], b[used] = small.a.cuda(), small.b.cuda()
+    plan = w8.lora_plan(small.lengths, [used[l] if l >= 0 else -1 for l in small.adapters], L)
+    _, u = w8.lora_forward(small.x.cuda(), a, b, plan, base=small.base.cuda())
+    da, db = torch.full((L, R, K), 7.0, device="cuda"), torch.full((L, N, R), 7.0, device="cuda")
+    dx, _, _ = w8.lora_backward(small.dy.cuda(), small.x.cuda(), u, a, b, plan, base=small.dbase.cuda(), da=da, db=db)
+    rx, ra, rb, ex, ea, eb = small.backward(u.cpu())
+    _near(dx, rx, ex, "dx")
+    _near(da[used], ra, ea, "da")
+    _near(db[used], rb, eb, "db")
+    da[used] = 0
+    db[used] = 0
+    assert not da.any() and not db.any()

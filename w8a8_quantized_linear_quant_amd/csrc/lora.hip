@@ -18,6 +18,8 @@
 //   the weight, 512 KB a workgroup from L2), up 84 us (403 MB, 4.8 TB/s)
 //   M 8192, K = N 4096, R 32, backward: down 17 us (67 MB), up 30 us (134 MB,
 //   4.5 TB/s), outer sums 31 us (134 MB, 4.3 TB/s), their splits added up 4.5 us
+#include <algorithm>
+
 #include "block.hpp"
 
 namespace w8a8 {
@@ -848,9 +850,9 @@ constexpr int outer_simd_waves(int JB) { return JB == 1 ? 5 : JB == 2 ? 3 : 2; }
 
 template <int JB>
 __global__ __launch_bounds__(64 * kOuterWaves, outer_simd_waves(JB)) void lora_outer_kernel(
-    OuterPair both, int64_t M, int L, int R, const int32_t *ranks, const int32_t *plan, int T, int splits) {
+    OuterPair both, int64_t M, int L, int R, const int32_t *ranks, const int32_t *plan, int T, int splits, int q0) {
     __shared__ __attribute__((aligned(16))) char ys[kTileRows * 256], vs[3][kTileRows * 32 * JB];
-    const int na = both.a.groups * L * splits, q = blockIdx.x;
+    const int na = both.a.groups * L * splits, q = q0 + blockIdx.x;
     if (q < na) outer_block<JB, true>(both.a, q, M, L, R, ranks, plan, T, splits, ys, vs);
     else outer_block<JB, false>(both.b, q - na, M, L, R, ranks, plan, T, splits, ys, vs);
 }
@@ -858,6 +860,10 @@ __global__ __launch_bounds__(64 * kOuterWaves, outer_simd_waves(JB)) void lora_o
 __global__ __launch_bounds__(256) void lora_sums_kernel(SplitSums sums) { add_splits(sums, blockIdx.x); }
 
 // ---------------------------------------------------------------- host side
+// Workgroups of a launch at most: with their threads far below HIP's 2^32.  A
+// call that needs more makes several launches, each of a part of the plan's tiles.
+constexpr int64_t kMaxBlocks = 1 << 20;
+
 int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 // v [M, R] = scale x w^T, w [L, R, C] or, TR, [L, C, R].
@@ -874,15 +880,18 @@ void down_launch(const uint16_t *x, int64_t M, int64_t C, int64_t ldx, const uin
     int blocks = rank_blocks(R), parts = 1;
     if (!two)
         while (blocks > 1 && (M / 16 + T) * parts * 2 <= 256) blocks /= 2, parts *= 2;
-    const int grid = (int)(two ? 2 * T : 4 * T) * parts;
+    const int per_tile = (two ? 2 : 4) * parts;
 #define W8A8_DOWN(JB, RB)                                                                                              \
-    lora_down_kernel<JB, RB, TR><<<grid, 64 * down_waves(JB, RB), 0, stream>>>(x, M, (int)C, ldx, w, (int)L, (int)R,   \
-                                                                              scale, ranks, plan, (int)T, parts, v)
-    switch (blocks) {
-    case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
-    case 2: two ? W8A8_DOWN(2, 2) : W8A8_DOWN(2, 1); break;
-    case 4: two ? W8A8_DOWN(4, 2) : W8A8_DOWN(4, 1); break;
-    default: two ? W8A8_DOWN(8, 2) : W8A8_DOWN(8, 1); break;
+    lora_down_kernel<JB, RB, TR><<<n * per_tile, 64 * down_waves(JB, RB), 0, stream>>>(                                \
+        x, M, (int)C, ldx, w, (int)L, (int)R, scale, ranks, plan + 4 * t0, n, parts, v)
+    for (int64_t t0 = 0; t0 < T; t0 += kMaxBlocks / per_tile) {
+        const int n = (int)std::min(T - t0, kMaxBlocks / per_tile);
+        switch (blocks) {
+        case 1: two ? W8A8_DOWN(1, 2) : W8A8_DOWN(1, 1); break;
+        case 2: two ? W8A8_DOWN(2, 2) : W8A8_DOWN(2, 1); break;
+        case 4: two ? W8A8_DOWN(4, 2) : W8A8_DOWN(4, 1); break;
+        default: two ? W8A8_DOWN(8, 2) : W8A8_DOWN(8, 1); break;
+        }
     }
 #undef W8A8_DOWN
 }
@@ -896,15 +905,20 @@ void up_launch(const float *v, const uint16_t *w, int64_t M, int64_t C, int64_t 
     // would leave less than two workgroups to a CU (300 rows, K 2048, N 5120, R
     // 32, both launches: 9.3 us against 10.5)
     const bool half = T * groups < 512;
-    const int grid = (int)(T * groups) * (half ? 2 : 1) + sums.blocks;
-#define W8A8_UP(JB, RB)                                                                                          \
-    lora_up_kernel<JB, TR, RB><<<grid, 64 * kUpWaves, 0, stream>>>(v, w, M, (int)C, (int)L, (int)R, ranks, plan, \
-                                                                   groups, base, ldbase, out, ldout, sums)
-    switch (rank_blocks(R)) {
-    case 1: half ? W8A8_UP(1, 2) : W8A8_UP(1, 4); break;
-    case 2: half ? W8A8_UP(2, 2) : W8A8_UP(2, 4); break;
-    case 4: half ? W8A8_UP(4, 2) : W8A8_UP(4, 4); break;
-    default: half ? W8A8_UP(8, 2) : W8A8_UP(8, 4); break;
+    const int per_tile = groups * (half ? 2 : 1);
+    const int64_t most = std::max<int64_t>(kMaxBlocks / per_tile, 1);
+#define W8A8_UP(JB, RB)                                                                                             \
+    lora_up_kernel<JB, TR, RB><<<n * per_tile + part.blocks, 64 * kUpWaves, 0, stream>>>(                           \
+        v, w, M, (int)C, (int)L, (int)R, ranks, plan + 4 * t0, groups, base, ldbase, out, ldout, part)
+    for (int64_t t0 = 0; t0 < T; t0 += most) {
+        const int n = (int)std::min(T - t0, most);
+        const SplitSums part = t0 == 0 ? sums : SplitSums{};
+        switch (rank_blocks(R)) {
+        case 1: half ? W8A8_UP(1, 2) : W8A8_UP(1, 4); break;
+        case 2: half ? W8A8_UP(2, 2) : W8A8_UP(2, 4); break;
+        case 4: half ? W8A8_UP(4, 2) : W8A8_UP(4, 4); break;
+        default: half ? W8A8_UP(8, 2) : W8A8_UP(8, 4); break;
+        }
     }
 #undef W8A8_UP
 }
@@ -1078,14 +1092,17 @@ extern "C" w8a8_status lora_backward(const uint16_t *dy, int64_t M, int64_t N, i
     if (da) {
         const OuterPair both = {{x, ldx, g, splits > 1 ? parts : da, (int)K, ga},
                                 {dy, lddy, u, splits > 1 ? parts + splits * na : db, (int)N, gb}};
-#define W8A8_OUTER(JB)                                                                                        \
-    lora_outer_kernel<JB><<<(int)grid, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan,   \
-                                                                     (int)T, (int)splits)
-        switch (rank_blocks(R)) {
-        case 1: W8A8_OUTER(1); break;
-        case 2: W8A8_OUTER(2); break;
-        case 4: W8A8_OUTER(4); break;
-        default: W8A8_OUTER(8); break;
+#define W8A8_OUTER(JB)                                                                                       \
+    lora_outer_kernel<JB><<<n, 64 * kOuterWaves, 0, stream>>>(both, M, (int)L, (int)R, ranks, plan, (int)T,  \
+                                                              (int)splits, (int)q0)
+        for (int64_t q0 = 0; q0 < grid; q0 += kMaxBlocks) {
+            const int n = (int)std::min(grid - q0, kMaxBlocks);
+            switch (rank_blocks(R)) {
+            case 1: W8A8_OUTER(1); break;
+            case 2: W8A8_OUTER(2); break;
+            case 4: W8A8_OUTER(4); break;
+            default: W8A8_OUTER(8); break;
+            }
         }
 #undef W8A8_OUTER
     }
