@@ -472,3 +472,49 @@ def test_dx_alone_of_very_many_rows(w8):
         rows = slice(i, min(i + 2 ** 24, M))
         w8.layer_norm_backward(dy[rows], x[rows], mu[rows], rs[rows], out=again[rows])
     assert torch.equal(again, dx)
+
+
+# ---------------------------------------------------------- the other variants
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2000, 2001, 14000, 16001, 16384])
+def test_the_widest_resident_rows(w8, K, xt):
+    _check(w8, 5, K, xt, "f32", seed=K)
+
+
+@pytest.mark.parametrize("weight", [False, True])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(3, 3), (70, 504), (9, 501), (70, 1000), (9, 1001), (70, 2040), (9, 2041), (70, 4088),
+                                 (9, 4089), (30, 8184), (9, 8185), (9, 16377), (3, 17001)])
+def test_dx_alone(w8, M, K, xt, weight):
+    """The input gradient without the parameters' (the default without a
+    weight), in each of its layouts, even widths and odd."""
+    print(f"[norm] dx alone M{M} K{K} {xt} weight={weight}", flush=True)
+    x, dy, w, _ = _inputs(M, K, xt, "f32", seed=M + K, weight=weight)
+    _, mu, rs = w8.layer_norm_forward(x.cuda())
+    dx, dw, db = w8.layer_norm_backward(dy.cuda(), x.cuda(), mu, rs, _cuda(w), need_params=False)
+    assert dw is None and db is None
+    rx, _, _, ex, _, _ = _grad_reference(dy, x, mu.cpu(), rs.cpu(), w)
+    _near(dx, rx, ex + ROUND[x.dtype] * (rx.abs() + ex), "dx")
+    if not weight:
+        assert torch.equal(w8.layer_norm_backward(dy.cuda(), x.cuda(), mu, rs)[0], dx)
+    over = dy.cuda()
+    assert torch.equal(w8.layer_norm_backward(over, x.cuda(), mu, rs, _cuda(w), out=over, need_params=False)[0], dx)
+
+
+@pytest.mark.parametrize("M,K,xt", [(70, 504, "bf16"), (1030, 2201, "f32"), (300, 8185, "bf16"), (70, 9001, "bf16")])
+def test_parameters_alone_and_one_of_them(w8, M, K, xt):
+    """dweight and dbias without dx, and through the C entry each by itself,
+    are the bits of the whole call."""
+    x, dy, w, b = (_cuda(t) for t in _inputs(M, K, xt, "f32", seed=K))
+    _, mu, rs = w8.layer_norm_forward(x, w, b)
+    _, dw, db = w8.layer_norm_backward(dy, x, mu, rs, w)
+    none, aw, ab = w8.layer_norm_backward(dy, x, mu, rs, w, need_dx=False)
+    assert none is None and torch.equal(aw, dw) and torch.equal(ab, db)
+    ws = torch.empty(w8.layer_norm_backward_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for first in (True, False):
+        got = torch.full((K,), 3.0, device="cuda")
+        st = w8.library().layer_norm_backward(
+            0 if xt == "bf16" else 1, dy.data_ptr(), K, x.data_ptr(), K, mu.data_ptr(), rs.data_ptr(), M, K, 1, w.data_ptr(),
+            None, 0, got.data_ptr() if first else None, None if first else got.data_ptr(), ws.data_ptr(), stream)
+        assert st == 0 and torch.equal(got, dw if first else db)

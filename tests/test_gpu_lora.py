@@ -566,3 +566,33 @@ def test_a_pool_beyond_one_launch(w8):
     da[used] = 0
     db[used] = 0
     assert not da.any() and not db.any()
+
+
+# ---------------------------------------------------------- the other variants
+@pytest.mark.parametrize("R", [8, 24, 64, 128])
+def test_sixty_four_rows_an_up_workgroup(w8, R):
+    """Enough tiles and columns, both ways, for an up-projection's workgroup to
+    take all 64 rows of a tile, its last ones in part."""
+    _check(w8, Batch([4100, 37, 4064], [1, -1, 0], 2056, 2104, R, 2, seed=R), f"64 rows R{R}")
+
+
+@pytest.mark.parametrize("R", [8, 16])
+@pytest.mark.parametrize("K,N", [(264, 4104), (4104, 264), (2056, 4104)])
+@pytest.mark.parametrize("S", [1, 30])
+def test_one_launch_of_several_column_groups(w8, S, K, N, R):
+    """Down- and up-projection in one launch where an output is wider than one
+    workgroup's columns: the further ones repeat the sums and leave u alone."""
+    lengths = [1] * (S - 1) + [5]
+    adapters = [i % 4 - 1 for i in range(S - 1)] + [2]
+    t = Batch(lengths, adapters, K, N, R, 3, seed=S + K)
+    _check(w8, t, f"{S} requests K{K} N{N} R{R}")
+    d = t.dev(w8)
+    want, wu = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **d)
+    base = t.base.cuda()
+    out, u = w8.lora_forward(t.x.cuda(), base=base, out=base, **d)
+    assert torch.equal(out, want) and torch.equal(u, wu)
+    alone, none = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), save_u=False, **d)
+    assert none is None and torch.equal(alone, want)
+    wdx = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=t.dbase.cuda(), **d)[0]
+    dbase = t.dbase.cuda()
+    assert torch.equal(w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=dbase, out=dbase, **d)[0], wdx)
