@@ -518,3 +518,15 @@ def test_parameters_alone_and_one_of_them(w8, M, K, xt):
             0 if xt == "bf16" else 1, dy.data_ptr(), K, x.data_ptr(), K, mu.data_ptr(), rs.data_ptr(), M, K, 1, w.data_ptr(),
             None, 0, got.data_ptr() if first else None, None if first else got.data_ptr(), ws.data_ptr(), stream)
         assert st == 0 and torch.equal(got, dw if first else db)
+
+
+def test_binding_refuses_what_is_no_tensor(w8):
+    x, dy, w, b = (_cuda(t) for t in _inputs(8, 64, "bf16", "bf16"))
+    mu = torch.zeros(8, device="cuda")
+    for args in ((x, [1.0]), (x, w, [1.0]), (x, None, 3.0), ([1.0],), (None,)):
+        for f in (w8.layer_norm_forward, w8.w8a8_quant_act_rowwise_layer_norm):
+            with pytest.raises(TypeError):
+                f(*args)
+    for args in ((dy, x, mu, mu, 3.0), (None, x, mu, mu), (dy, x, 1.0, mu)):
+        with pytest.raises(TypeError):
+            w8.layer_norm_backward(*args)

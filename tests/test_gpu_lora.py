@@ -596,3 +596,19 @@ def test_one_launch_of_several_column_groups(w8, S, K, N, R):
     wdx = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=t.dbase.cuda(), **d)[0]
     dbase = t.dbase.cuda()
     assert torch.equal(w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=dbase, out=dbase, **d)[0], wdx)
+
+
+def test_binding_refuses_what_is_no_tensor(w8):
+    t = Batch([10, 6], [0, 1], 64, 72, 16, 2)
+    d = t.dev(w8)
+    x, dy, u = t.x.cuda(), t.dy.cuda(), torch.zeros(16, 16, device="cuda")
+    for name in ("a", "b", "scale", "ranks"):
+        for bad in ([1.0], 3, "a"):
+            kw = dict(d, **{name: bad})
+            with pytest.raises(TypeError):
+                w8.lora_forward(x, **kw)
+            with pytest.raises(TypeError):
+                w8.lora_backward(dy, x, u, **kw)
+    for name in ("a", "b"):
+        with pytest.raises(TypeError):
+            w8.lora_forward(x, **dict(d, **{name: None}))

@@ -562,6 +562,8 @@ def lora_backward_workspace_bytes(M, T, K, N, R, L):
 def _lora_args(rows, dev, a, b, plan, scale, ranks):
     if not isinstance(plan, LoraPlan):
         raise TypeError("plan must be a LoraPlan (lora_plan)")
+    if not isinstance(a, _Tensor) or not isinstance(b, _Tensor):
+        raise TypeError("a and b must be torch.Tensors")
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
         raise ValueError(f"a must be [L, R, K] and b [L, N, R], got {tuple(a.shape)} and {tuple(b.shape)}")
     L, R, K = a.shape
@@ -635,6 +637,8 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def _dtype_of(t, name):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
@@ -649,7 +653,7 @@ def _norm_args(x, weight, bias):
     p = weight if weight is not None else bias
     if p is None:
         return dev, M, K, xt, px, ldx, xt, None, None
-    wt = _dtype_of(p, "weight")
+    wt = _dtype_of(p, "weight" if weight is not None else "bias")
     pw, pb = _vec(weight, K, p.dtype, dev, "weight"), _vec(bias, K, p.dtype, dev, "bias")
     return dev, M, K, xt, px, ldx, wt, pw, pb
 
