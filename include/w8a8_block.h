@@ -63,7 +63,8 @@ w8a8_status lora_plan(const int64_t *lengths, const int32_t *adapters, int64_t S
  * u[m, j]   = scale[l] * sum_k x[m, k] * a[l, j, k]   for j < ranks[l], else 0
  * for every row m of a tile with adapter l; rows without an adapter have
  * u = 0 and out = base.  f32 sums; u is multiplied into b as a pair of bf16
- * halves (~16 significant bits).
+ * halves (~16 significant bits; what lies below 2^-133, bf16's smallest step,
+ * counts as 0).
  *   x bf16 [M, ldx] (first K columns); a bf16 [L, R, K]; b bf16 [L, N, R];
  *   scale f32 [L] or NULL (1); ranks int32 [L] or NULL (R), clamped to
  *   [0, R]: entries of a and b beyond an adapter's rank are never used,
@@ -92,7 +93,8 @@ w8a8_status lora_forward(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, c
  *   dy bf16 [M, lddy]; x, a, b, scale, ranks, plan as in the forward call;
  *   u f32 [M, R] from it.  base bf16 [M, ldbase] or NULL: the shared
  *   projection's own input gradient (w8a8_linear_backward_dx), may be dx.
- *   dx bf16 [M, lddx]; da f32 [L, R, K]; db f32 [L, N, R], f32 accurate.
+ *   dx bf16 [M, lddx]; da f32 [L, R, K]; db f32 [L, N, R], f32 accurate (g and
+ *   u are three bf16 parts: all 24 bits of values above 2^-110).
  *   dx may be NULL (no input gradient); da and db may both be NULL.
  *   workspace lora_backward_workspace_bytes(M, T, K, N, R, L) bytes.
  * Shape rules as lora_forward.

@@ -22,7 +22,10 @@ constexpr int kStreamSplits = 64;    // row splits of the streaming column sums
 // 16384 wide: 2^24 of them, a workgroup each, fit no memory.)
 constexpr int64_t kMaxGrid = 1 << 22;
 
-// One workgroup per row, the row read again for each pass.
+// Rows too wide for registers: one workgroup per row, the row read again for
+// each pass, an element at a time (2048 rows of 20000 bf16: the norm 130 us, to
+// codes 171 us, the backward pass 57 + 146 + 5 us; a floor of 31, 23 and 46 us
+// at the rate of a large copy).
 template <class X>
 __device__ __forceinline__ void row_stats(const typename X::type *x, int K, float eps, float *part, float &mean,
                                           float &rstd) {
@@ -93,10 +96,13 @@ __device__ __forceinline__ uint32_t codes4(const float *v, const RowScale &s) {
 // Rows that fit the registers of one workgroup are read once: W waves share a
 // row, thread t of the row's 64 W holds its chunks t, t + 64 W, ... (16 bytes
 // each).  A workgroup takes several rows, the next one's loads in flight while a
-// row is worked on, the weights in registers.  Bound by memory in f32 (8192
-// rows of 4096: 48 us, 5.6 TB/s with what the caches keep) and nearly so in bf16
-// (25.6 us, 5.2 TB/s); to codes by memory and about 25 vector instructions an
-// element alike (22.9 us, 4.4 TB/s).
+// row is worked on, the weights in registers.  Bound by memory: 8192 rows of
+// 4096 in f32 43.7 us (268 MB, 6.1 TB/s with what the caches keep), in bf16
+// 23.2 us (134 MB, 5.8 TB/s); to codes by memory and about 25 vector instructions
+// an element alike (bf16 24.8 us, 101 MB, 4.1 TB/s).  (These and the backward
+// kernel's times: medians under rocprofv3, inputs rotated over three sets.  The
+// comparisons of layouts further down: inputs rotated over more memory than the
+// caches hold, the launches of a call together.)
 // OUT: what leaves (the norm in X's type, int8 codes or e4m3 codes).  EVEN: K
 // is a whole number of chunks, so that a chunk is either there or not.
 enum { kOutNorm = 0, kOutInt8 = 1, kOutE4m3 = 2 };
@@ -374,9 +380,10 @@ constexpr int backward_threads(int ept) { return ept <= 8 ? 1024 : 512; }
 
 // As the forward kernel, and each thread keeps the sums over its workgroup's
 // rows of dy h and dy for its own columns.  A workgroup of `groups` row groups
-// takes every gridDim.x * groups-th row (8192 x 4096 bf16: 38 us for 201 MB, 5 TB/s);
-// the next row's loads are in flight while a row is worked on.  At the end the groups' sums meet in LDS and leave
-// as partials [workgroup][dw, db][position]; ln_reduce_kernel adds them.
+// takes every gridDim.x * groups-th row (8192 x 4096: bf16 37.5 us for 201 MB,
+// 5.4 TB/s; f32 74.7 us for 403 MB); the next row's loads are in flight while a
+// row is worked on.  At the end the groups' sums meet in LDS and leave as partials
+// [workgroup][dw, db][position]; ln_reduce_kernel adds them.
 // Position p of column c = (i T + t) V + e:  p = (i V + e) T + t.
 template <class X, int WT, bool EVEN, int W, int NCH, bool PARAMS>
 __global__ __launch_bounds__(backward_threads(NCH * X::kVec)) void ln_backward_kernel(
@@ -594,8 +601,9 @@ Layout backward_layout(int64_t K) {
         if (K <= 64 * W * 8) return {W, 8};
     return {0, 0};
 }
-// The input gradient alone keeps no sums: 16 elements per thread (the same
-// rows: 38.5 us against 47.2 with 8), 32 for the widest.
+// The input gradient alone keeps no sums: 16 elements per thread (8192 rows of
+// 2048: 18.9 us against 26.8 with 8; of 4096: 36.4 against 38.1), 32 for the
+// widest.
 Layout backward_dx_layout(int64_t K) {
     if (K <= 512) return {1, 8};
     for (int W = 1; W <= 8; W *= 2)

@@ -4,20 +4,24 @@
 //   u = s_l x A_l^T           (down, over K)       out = base + u B_l^T   (up)
 //   g = s_l dy B_l            (down, over N)       dx  = base + g A_l     (up)
 //   dA_l = sum_m g^T x        dB_l = sum_m dy^T u  (over the rows of l)
-// Three kernels in all, each on the bf16 MFMA: a down-projection of the rows,
-// an up-projection added to a base, and a sum of outer products over an
-// adapter's rows.  The weight of the first two is A [R, K] or B [N, R]: one of
-// the two has the MFMA's contraction index contiguous in memory, the other
-// (TR) is transposed on its way to the registers.
+// The kernels, on the bf16 MFMA: a down-projection of the rows, an up-projection
+// added to a base, both in one for few rows and ranks, and a sum of outer
+// products over an adapter's rows.  (The splits of these sums are added up in
+// the up-projection's launch, or in one of their own where there is none.)  The
+// weight of the projections is A [R, K] or B [N, R]: one of the two has the
+// MFMA's contraction index contiguous in memory, the other (TR) is transposed on
+// its way to the registers.
 //
-// All three are bound by streaming the wide tensors (x, dy, base, out): R is
-// small, so each takes 2 R operations for the 2 bytes of an element, far below
-// the 500 or so at which the matrix pipes would be the bound.  Measured (MI355X,
-// a large copy moves 5.3 TB/s; kernel times under rocprofv3, inputs rotated):
-//   M 8192, K 4096, N 12288, R 64, forward: down 26 us (67 MB of x; the rest is
-//   the weight, 512 KB a workgroup from L2), up 84 us (403 MB, 4.8 TB/s)
-//   M 8192, K = N 4096, R 32, backward: down 17 us (67 MB), up 30 us (134 MB,
-//   4.5 TB/s), outer sums 31 us (134 MB, 4.3 TB/s), their splits added up 4.5 us
+// All are bound by streaming the wide tensors (x, dy, base, out): R is small, so
+// each takes 2 R operations for the 2 bytes of an element, far below the 500 or
+// so at which the matrix pipes would be the bound.  Measured (MI355X, a large
+// copy moves 5.3 TB/s; medians under rocprofv3, inputs rotated over three sets):
+//   M 8192, K 4096, N 12288, R 64, forward: down 28 us (67 MB of x; the rest is
+//   the weight, 512 KB a workgroup from L2), up 83 us (403 MB, 4.8 TB/s)
+//   M 8192, K = N 4096, R 32, backward: down 18.6 us (67 MB), outer sums 32 us
+//   (134 MB, 4.2 TB/s), up with their splits 29.6 us (134 MB, 4.5 TB/s)
+// The comparisons at the single choices below are of one set of inputs taken over
+// and over, part of which the caches hold.
 #include <algorithm>
 
 #include "block.hpp"
@@ -118,8 +122,9 @@ __device__ __forceinline__ v4u transposed_fragment(const char *area, int jb, int
 }
 
 // acc += this wave's slices of rows x weight, for the 16 RB rows from `first`
-// of a tile and the 16 JB ranks from j0; area: the wave's LDS; block: which workgroup asks (all that share
-// a result must give the same, for the order of its sums).
+// of a tile and the 16 JB ranks from j0; area: the wave's LDS; block: which
+// workgroup asks (all that share a result must give the same, for the order of
+// its sums).
 template <int JB, int RB, bool TR, int W>
 __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x, const Tile &tile, int first, int C,
                                           int64_t ldx, const uint16_t *w, int R, int j0, char *area, unsigned block) {
@@ -129,7 +134,7 @@ __device__ __forceinline__ void down_sums(v4f (&acc)[RB][JB], const uint16_t *x,
     const auto rx = rows_rsrc(x, tile.row0 + first, tile.rows - first, ldx, C);
     const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(w) + (int64_t)tile.adapter * R * C, (short)0,
                                                       R * C * 2, kBufferRsrcWord3);
-            const int li = lane >> 4, lc = (lane & 15) * 8;  // row and column of a lane in a load of 4 rows x 128
+    const int li = lane >> 4, lc = (lane & 15) * 8;  // row and column of a lane in a load of 4 rows x 128
     // past C both factors read 0: neither may be whatever lies behind a row
     auto fetch_x = [&](int slice, int a, v4u (&d)[4]) {
         const int k = slice * kSlice + lc;
@@ -450,7 +455,8 @@ __device__ __forceinline__ void up_again(unsigned again, __amdgpu_buffer_rsrc_t 
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (4 * fg + e < rows - first && c < C) *reinterpret_cast<v4u *>(out + (first + 4 * fg + e) * ldout + c) = d[e];
+            if (4 * fg + e < rows - first && c < C)
+                *reinterpret_cast<v4u *>(out + (first + 4 * fg + e) * ldout + c) = d[e];
     }
 }
 
@@ -485,11 +491,9 @@ __device__ __forceinline__ void add_splits(const SplitSums &sums, int block) {
 }
 
 template <int JB, bool TR, int RB>
-__global__ __launch_bounds__(64 * kUpWaves, up_simd_waves(JB, RB)) void lora_up_kernel(const float *v, const uint16_t *w, int64_t M, int C,
-                                                                int L, int R, const int32_t *ranks,
-                                                                const int32_t *plan, int groups, const uint16_t *base,
-                                                                int64_t ldbase, uint16_t *out, int64_t ldout,
-                                                                SplitSums sums) {
+__global__ __launch_bounds__(64 * kUpWaves, up_simd_waves(JB, RB)) void lora_up_kernel(
+    const float *v, const uint16_t *w, int64_t M, int C, int L, int R, const int32_t *ranks, const int32_t *plan,
+    int groups, const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldout, SplitSums sums) {
     if ((int)blockIdx.x < sums.blocks) return add_splits(sums, blockIdx.x);
     constexpr int KB = JB == 1 ? 1 : JB / 2;  // 32-wide contractions
     constexpr int P = JB * 16 + 8;  // halves of an LDS row: 16 rows' reads fall on distinct banks
@@ -560,8 +564,9 @@ __global__ __launch_bounds__(64 * kUpWaves, up_simd_waves(JB, RB)) void lora_up_
 // columns a wave: one launch, with base and the up-projection's weights loaded
 // ahead of the sums, ranks up to 16.  Where 2048 columns a workgroup do not
 // cover C2, each further one takes the sums again (`groups` workgroups a block
-// of rows).  Bound by the latency of its chain of loads: 4.8 us for one row at
-// C = C2 1024, 9.2 for 48 requests' rows at 4096 (8.6 MB of weights).
+// of rows).  Bound by the latency of its chain of loads: 4.9 us for one row at
+// C = C2 1024, 9.1 for 48 requests' rows at 4096 (8.6 MB of weights, which the
+// caches do not hold; 7.7 where they do).
 template <bool TR>
 __global__ __launch_bounds__(1024) void lora_both_kernel(const uint16_t *x, int64_t M, int C, int64_t ldx,
                                                          const uint16_t *w, int L, int R, const float *scale,
@@ -679,8 +684,8 @@ __device__ __forceinline__ v4u read_transposed(const char *area, int m0, int pie
 // the 128 x 16 JB output, from pieces pc and pj.  FINITE: v's second and third
 // parts meet the finite entries of y alone.
 template <int JB, bool RANKS_FIRST, bool FINITE, int NC, int NJ>
-__device__ __forceinline__ void outer_sums(v4f (&acc)[NC][NJ], const Outer &o, int col0, int pc, int pj, int64_t M, int L,
-                                           int R, const int32_t *plan, int begin, int end, char *ys,
+__device__ __forceinline__ void outer_sums(v4f (&acc)[NC][NJ], const Outer &o, int col0, int pc, int pj, int64_t M,
+                                           int L, int R, const int32_t *plan, int begin, int end, char *ys,
                                            char (&vs)[3][kTileRows * 32 * JB]) {
     constexpr int kThreads = 64 * kOuterWaves;
     const int lane = threadIdx.x & 63;
