@@ -612,3 +612,36 @@ def test_binding_refuses_what_is_no_tensor(w8):
     for name in ("a", "b"):
         with pytest.raises(TypeError):
             w8.lora_forward(x, **dict(d, **{name: None}))
+
+
+@pytest.mark.parametrize("case", [(40, 264, 328, 8), (70, 264, 328, 32), (300, 264, 328, 128), (8300, 72, 2056, 16),
+                                  (8300, 72, 2056, 64), (8300, 72, 2056, 128)], ids=lambda c: "M%d-K%d-N%d-R%d" % c)
+def test_non_finite_values_of_base_stay_where_they_are(w8, case):
+    """NaN and infinities in base: in out at the same places, every other
+    element the bits of a base without them; rows with an adapter, without one
+    and with a rank of 0, in place too."""
+    M, K, N, R = case
+    print(f"[lora] non-finite base {case}", flush=True)
+    n = M // 3
+    t = Batch([n, n, M - 2 * n], [0, -1, 1], K, N, R, 2, ranks=[R - 1, 0], seed=M + R)
+    d = t.dev(w8)
+    want, u = w8.lora_forward(t.x.cuda(), base=t.base.cuda(), **d)
+    wdx, wa, wb = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=t.dbase.cuda(), **d)
+    for cols, clean, grad in ((N, want, False), (K, wdx, True)):
+        g = torch.Generator().manual_seed(R)
+        at = torch.rand(M, cols, generator=g) < 3 / cols
+        at[1], at[n + 1], at[2 * n + 1] = False, False, False
+        bad = torch.where(torch.rand(M, cols, generator=g) < 0.5, float("nan"), float("-inf")).bfloat16()
+        base = torch.where(at, bad, t.dbase if grad else t.base).cuda()
+        for inplace in (False, True):
+            b = base.clone()
+            out = b if inplace else None
+            if grad:
+                got, ga, gb = w8.lora_backward(t.dy.cuda(), t.x.cuda(), u, base=b, out=out, **d)
+                assert torch.equal(ga, wa) and torch.equal(gb, wb)
+            else:
+                got, gu = w8.lora_forward(t.x.cuda(), base=b, out=out, **d)
+                assert torch.equal(gu, u)
+            got = got.cpu()
+            assert torch.equal(got[~at], clean.cpu()[~at])
+            assert torch.equal(got[at].isnan(), bad[at].isnan()) and torch.equal(got[at].isneginf(), bad[at].isneginf())

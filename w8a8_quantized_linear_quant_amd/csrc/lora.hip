@@ -364,7 +364,8 @@ __device__ __forceinline__ v4u v_fragment(const uint16_t (*hi)[P], const uint16_
 
 // One block of 16 rows of a wave's 128 columns: base (bf) plus v (its halves in
 // LDS rows hi, lo of this block) times the weight, stored, unless a lane holds a
-// NaN in it: returns whether.  (Looking costs 16 instructions.)
+// NaN in it: returns whether.  (Looking costs 16 instructions.  With a rank of 0
+// the block is base, and there is no weight to take it again with.)
 template <int JB, int KB, int P>
 __device__ __forceinline__ bool up_rows(const v4u (&bf)[4], const uint16_t (*hi)[P], const uint16_t (*lo)[P],
                                         const v4u (&wf)[8][KB], int r, uint16_t *out, int64_t ldout, int rows, int col0,
@@ -393,10 +394,10 @@ __device__ __forceinline__ bool up_rows(const v4u (&bf)[4], const uint16_t (*hi)
     for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            any = max_or_nan(any, max_or_nan(acc[2 * p][e], acc[2 * p + 1][e]));
+            any = max_or_nan(max_or_nan(any, acc[2 * p][e]), acc[2 * p + 1][e]);
             d[e][p] = pack_bf16x2(acc[2 * p][e], acc[2 * p + 1][e]);
         }
-    if (__builtin_expect(__any(any != any && c < C), false)) return false;
+    if (__builtin_expect(r > 0 && __any(any != any && c < C), false)) return false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int row = 4 * fg + e;
