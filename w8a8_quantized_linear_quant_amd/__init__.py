@@ -21,6 +21,11 @@ the current stream.  The functions carry the C names:
   lora_forward / lora_backward  adapters of many requests added to a shared projection, and their gradients
   layer_norm_forward / layer_norm_backward   layer norm over rows, and its gradients
   w8a8_quant_act_rowwise_layer_norm   row-wise activation quantization of the layer norm, in one pass
+  mxfp4_quantize / mxfp4_quantize_transposed / mxfp4_dequantize   the microscaled 4-bit format
+  mxfp4_linear / mxfp4_linear_backward_dx   4-bit product -> bf16, and its input gradient
+  w8a8_quant_weight_grouped     tensor-wise quantization of each weight of a group of them (experts)
+  w8a8_linear_grouped / mxfp4_linear_grouped   products of groups of rows with a weight each, rows gathered -> bf16
+  w8a8_linear_grouped_backward_dx / mxfp4_linear_grouped_backward_dx   their input gradients
   probe_mfma_i8                 diagnostic: sustained int8 MFMA loop (include/w8a8_probe.h)
   probe_cvt_e4m3                diagnostic: the hardware e4m3 conversion on consecutive f32 bit patterns
   probe_gemm_tile_n             diagnostic: the tile width along N w8a8_linear picks for an M x N output
@@ -44,6 +49,7 @@ FP8_E4M3 = 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8.h")
 BLOCK_HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8_block.h")
+EXPERTS_HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8_experts.h")
 PROBE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "w8a8_probe.h")
 
 
@@ -89,6 +95,16 @@ def _load_library():
         "layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
         "layer_norm_backward": (I, [I, P, I64, P, I64, P, P, I64, I64, I, P, P, I64, P, P, P, P]),
         "w8a8_quant_act_rowwise_layer_norm": (I, [I, I, P, I64, I64, I64, I, P, P, F, P, I64, P, P, P, P]),
+        "mxfp4_scale_stride": (I64, [I64]),
+        "mxfp4_quantize": (I, [I, P, I64, I64, I64, P, I64, P, P]),
+        "mxfp4_quantize_transposed": (I, [I, P, I64, I64, I64, I64, P, I64, P, P]),
+        "mxfp4_dequantize": (I, [P, P, I64, I64, I64, I, P, I64, P]),
+        "mxfp4_linear": (I, [P, P, P, P, P, I64, I64, I64, P, P]),
+        "mxfp4_linear_backward_dx": (I, [P, P, P, P, I64, I64, I64, P, P]),
+        "w8a8_linear_grouped": (I, [I, P, I64, P, P, P, I, P, P, I64, P, I64, I64, I64, P, P]),
+        "w8a8_linear_grouped_backward_dx": (I, [I, P, P, P, P, P, I64, I64, I64, I64, P, P]),
+        "mxfp4_linear_grouped": (I, [P, I64, P, P, P, P, P, I64, P, I64, I64, I64, P, P]),
+        "mxfp4_linear_grouped_backward_dx": (I, [P, P, P, P, P, I64, I64, I64, I64, P, P]),
         "w8a8_probe_sink_count": (I64, []),
         "w8a8_probe_mfma_i8": (I, [P, P, I64, P, P]),
         "w8a8_probe_cvt_e4m3": (I, [ctypes.c_uint32, I64, P, P]),
@@ -724,6 +740,224 @@ def w8a8_quant_act_rowwise_layer_norm(x, weight=None, bias=None, eps=1e-5, qtype
         qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, _vec(scale, M, _F32, dev, "scale"),
         _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd"), _stream(dev)))
     return xq, _first(scale, M)
+
+
+# ------------------------------------------------ the microscaled 4-bit format
+_U8 = torch.uint8
+
+
+def mxfp4_scale_stride(K):
+    """Bytes from one row's scales to the next one's."""
+    return -(-K // 512) * 16
+
+
+def mxfp4_quantize(x, ldq=None, out=None, scale=None):
+    """x bf16 or f32 [..., K] (a matrix may have a row stride, of any alignment).  Returns (codes uint8 [..., ldq / 2],
+    two a byte, the even column in the low half; scales uint8 [..., mxfp4_scale_stride(ldq)], e + 127 for 2^e).
+    ldq: K rounded up to a multiple of 32 by default."""
+    xt = _dtype_of(x, "x")
+    lead = x.shape[:-1]
+    if x.dim() != 2:
+        if x.dim() < 2 or not x.is_contiguous():
+            raise ValueError("x must be a matrix, or contiguous with more dimensions")
+        x = x.view(-1, x.shape[-1])
+    dev = _gpu_matrix(x, "x")
+    M, K = x.shape
+    px, ldx = _view(x, M, K, x.dtype, dev, "x", align=False)
+    ldq = ldq if ldq is not None else K + (-K) % 32
+    out = _out(out, (*lead, ldq // 2), _U8, dev, "out")
+    scale = _out(scale, (*lead, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
+    _check(_lib.mxfp4_quantize(xt, px, M, K, ldx, out.data_ptr(), ldq, scale.data_ptr(), _stream(dev)))
+    return out, scale
+
+
+def mxfp4_quantize_transposed(w, ldq=None, out=None, scale=None):
+    """mxfp4_quantize of the transpose(s) of w bf16 or f32 [N, K] (may have a row stride) or [B, N, K] (contiguous):
+    codes uint8 [K, ldq / 2] or [B, K, ldq / 2], blocks along N, and scales.  The weight of the input gradient."""
+    wt = _dtype_of(w, "w")
+    if not w.is_cuda:
+        raise ValueError("w must be a GPU tensor")
+    if w.dim() == 3:
+        if not w.is_contiguous():
+            raise ValueError("w must be contiguous with three dimensions")
+        lead, (N, K) = (w.shape[0],), w.shape[1:]
+        if w.data_ptr() % 16 != 0:
+            raise ValueError("w must start on a 16-byte boundary")
+        pw, ldx = w.data_ptr(), K
+    else:
+        _gpu_matrix(w, "w")
+        lead, (N, K) = (), w.shape
+        pw, ldx = _view(w, N, K, w.dtype, w.device, "w", align=False)
+    dev = w.device
+    ldq = ldq if ldq is not None else N + (-N) % 32
+    out = _out(out, (*lead, K, ldq // 2), _U8, dev, "out")
+    scale = _out(scale, (*lead, K, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
+    _check(_lib.mxfp4_quantize_transposed(wt, pw, lead[0] if lead else 1, N, K, ldx, out.data_ptr(), ldq,
+                                          scale.data_ptr(), _stream(dev)))
+    return out, scale
+
+
+def mxfp4_dequantize(codes, scale, K=None, dtype=torch.bfloat16, out=None):
+    """The values of codes uint8 [..., ldq / 2] with their scales: dtype (bf16 or f32) [..., K], K = ldq by default.
+    `out` (two dimensions) may have a row stride."""
+    dev, lead, ldq = _mx_operand(codes, scale, "codes", "scale")
+    K = ldq if K is None else K
+    M = codes.numel() * 2 // ldq if ldq else 0
+    if out is None:
+        out = torch.empty((*lead, K), dtype=dtype, device=dev)
+    yt = _dtype_of(out, "out")
+    if len(lead) == 1:
+        py, ldy = _view(out, M, K, out.dtype, dev, "out", align=False)
+    else:
+        py, ldy = _out(out, (*lead, K), out.dtype, dev, "out").data_ptr(), K
+    _check(_lib.mxfp4_dequantize(codes.data_ptr(), scale.data_ptr(), M, K, ldq, yt, py, ldy, _stream(dev)))
+    return out
+
+
+def _mx_operand(codes, scale, cname, sname, device=None):
+    """Checks a pair of codes [..., K / 2] and scales: (device, leading shape, K)."""
+    if not isinstance(codes, _Tensor) or not isinstance(scale, _Tensor):
+        raise TypeError(f"{cname} and {sname} must be torch.Tensors")
+    if codes.dtype is not _U8 or scale.dtype is not _U8:
+        raise TypeError(f"{cname} and {sname} must be torch.uint8, got {codes.dtype} and {scale.dtype}")
+    dev = codes.device
+    if not codes.is_cuda:
+        raise ValueError(f"{cname} must be a GPU tensor")
+    if scale.device != dev or (device is not None and dev != device):
+        raise ValueError(f"{cname} is on {dev}, {sname} on {scale.device}" +
+                         (f", the other operands on {device}" if device is not None else ""))
+    if codes.dim() < 2 or not codes.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"{cname} and {sname} must be contiguous, of two dimensions or more")
+    K = 2 * codes.shape[-1]
+    want = (*codes.shape[:-1], mxfp4_scale_stride(K))
+    if scale.shape != want:
+        raise ValueError(f"{sname} must have shape {tuple(want)} beside {cname} {tuple(codes.shape)}, "
+                         f"got {tuple(scale.shape)}")
+    return dev, codes.shape[:-1], K
+
+
+def mxfp4_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
+    """4-bit linear: xq [M, K / 2], wq [N, K / 2] with their scales (mxfp4_quantize) -> bf16 [M, N]."""
+    dev, lead, K = _mx_operand(xq, x_scale, "xq", "x_scale")
+    _, wlead, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
+    if len(lead) != 1 or len(wlead) != 1 or wk != K:
+        raise ValueError(f"xq must be [M, K / 2] and wq [N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
+    M, N = lead[0], wlead[0]
+    pb = _vec(bias, N, _BF16, dev, "bias")
+    y = _out(out, (M, N), _BF16, dev, "out")
+    _check(_lib.mxfp4_linear(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, M, N, K,
+                             y.data_ptr(), _stream(dev)))
+    return y
+
+
+def mxfp4_linear_backward_dx(dyq, dy_scale, wq_t, w_scale_t, out=None):
+    """dX = dY . W: dyq [M, N / 2] (mxfp4_quantize of dY), wq_t [K, N / 2] (mxfp4_quantize_transposed of W) with their
+    scales -> bf16 [M, K]."""
+    return mxfp4_linear(dyq, dy_scale, wq_t, w_scale_t, out=out)
+
+
+# ------------------------------------------------------- products of groups
+def w8a8_quant_weight_grouped(w, qtype=INT8, transposed=False):
+    """w8a8_quant_weight_tensorwise of each of w bf16 [E, N, K].  Returns (codes [E, N, K], codes^T [E, K, N] or None,
+    scales f32 [E])."""
+    cd = _code_dtype(qtype)
+    _need(w, _BF16, "w")
+    if w.dim() != 3:
+        raise ValueError(f"w must be 3-D, got {w.dim()}-D")
+    E, N, K = w.shape
+    wq = torch.empty((E, N, K), dtype=cd, device=w.device)
+    wq_t = torch.empty((E, K, N), dtype=cd, device=w.device) if transposed else None
+    scale = torch.empty((E, 4), dtype=_F32, device=w.device)       # each starts on a 16-byte boundary
+    ws = torch.empty(max(w8a8_weight_workspace_bytes(N, K), 1), dtype=_U8, device=w.device)
+    for e in range(E):
+        w8a8_quant_weight_tensorwise(w[e], qtype, out=wq[e], out_t=None if wq_t is None else wq_t[e], scale=scale[e],
+                                     workspace=ws)
+    return wq, wq_t, scale[:, 0].contiguous()
+
+
+def _groups(offsets, E, rows, bias, N, dev):
+    """(pointer of offsets, pointer of rows, rows of the output or None, pointer of bias)."""
+    if not isinstance(offsets, _Tensor) or offsets.dtype is not _I32:
+        raise TypeError("offsets must be a torch.int32 tensor")
+    if offsets.device != dev or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be contiguous, on {dev}, of shape {(E + 1,)}, got {tuple(offsets.shape)}")
+    pr, M = None, None
+    if rows is not None:
+        pr = _vec(rows, 0, _I32, dev, "rows")
+        if rows.dim() != 1:
+            raise ValueError(f"rows must be 1-D, got {rows.dim()}-D")
+        M = rows.shape[0]
+    if bias is not None and isinstance(bias, _Tensor) and bias.shape != (E, N):
+        raise ValueError(f"bias must have shape {(E, N)}, got {tuple(bias.shape)}")
+    return offsets.data_ptr(), pr, M, _vec(bias, E * N, _BF16, dev, "bias")
+
+
+def _codes8(t, dims, name, dtype=None, device=None):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must hold {dtype} codes, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {dims}-D, got shape {tuple(t.shape)}")
+    return t.device
+
+
+def w8a8_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None, out=None):
+    """Products of groups of rows with a weight each.  xq [X, K], wq [E, N, K] codes (same dtype); x_scale f32 [X];
+    w_scale f32 [E] or [E, N]; offsets int32 [E + 1]: output rows offsets[g] .. offsets[g + 1] - 1 take weight g;
+    rows int32 [M] or None: the row of xq that each output row takes; bias bf16 [E, N].  Returns bf16 [M, N]; rows in
+    no group are not written."""
+    qt = _qtype_of(xq) if isinstance(xq, _Tensor) else None
+    dev = _codes8(xq, 2, "xq")
+    _codes8(wq, 3, "wq", xq.dtype, dev)
+    X, K = xq.shape
+    E, N = wq.shape[:2]
+    if wq.shape[2] != K:
+        raise ValueError(f"xq and wq must share K, got {K} and {wq.shape[2]}")
+    po, pr, M, pb = _groups(offsets, E, rows, bias, N, dev)
+    M = X if M is None else M
+    ps = _vec(x_scale, X, _F32, dev, "x_scale")
+    per_channel = isinstance(w_scale, _Tensor) and w_scale.dim() == 2
+    if isinstance(w_scale, _Tensor) and w_scale.shape != ((E, N) if per_channel else (E,)):
+        raise ValueError(f"w_scale must have shape {(E,)} or {(E, N)}, got {tuple(w_scale.shape)}")
+    pw = _vec(w_scale, E, _F32, dev, "w_scale")
+    y = _out(out, (M, N), _BF16, dev, "out")
+    _check(_lib.w8a8_linear_grouped(qt, xq.data_ptr(), X, ps, wq.data_ptr(), pw, per_channel, pb, po, E, pr, M, N, K,
+                                    y.data_ptr(), _stream(dev)))
+    return y
+
+
+def w8a8_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale, offsets, out=None):
+    """dX[p] = dY[p] . W[g]: dyq [M, N] codes, wq_t [E, K, N] transposed weight codes, w_scale f32 [E] -> bf16 [M, K]
+    in the groups' order."""
+    if isinstance(w_scale, _Tensor) and w_scale.dim() != 1:
+        raise ValueError("w_scale must be [E]: a scale for each output channel does not leave the gradient's sum")
+    return w8a8_linear_grouped(dyq, dy_scale, wq_t, w_scale, offsets, out=out)
+
+
+def mxfp4_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None, out=None):
+    """w8a8_linear_grouped in the 4-bit format: xq [X, K / 2], wq [E, N, K / 2] with their scales (mxfp4_quantize)."""
+    dev, lead, K = _mx_operand(xq, x_scale, "xq", "x_scale")
+    _, wlead, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
+    if len(lead) != 1 or len(wlead) != 2 or wk != K:
+        raise ValueError(f"xq must be [X, K / 2] and wq [E, N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
+    X, (E, N) = lead[0], wlead
+    po, pr, M, pb = _groups(offsets, E, rows, bias, N, dev)
+    M = X if M is None else M
+    y = _out(out, (M, N), _BF16, dev, "out")
+    _check(_lib.mxfp4_linear_grouped(xq.data_ptr(), X, x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, po, E,
+                                     pr, M, N, K, y.data_ptr(), _stream(dev)))
+    return y
+
+
+def mxfp4_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale_t, offsets, out=None):
+    """dX[p] = dY[p] . W[g]: dyq [M, N / 2], wq_t [E, K, N / 2] (mxfp4_quantize_transposed) with their scales ->
+    bf16 [M, K] in the groups' order."""
+    return mxfp4_linear_grouped(dyq, dy_scale, wq_t, w_scale_t, offsets, out=out)
 
 
 # ---------------------------------------------------------------- diagnostics

@@ -1,0 +1,317 @@
+// mxfp4.hip -- quantizers and dequantizer of the microscaled 4-bit format.
+//
+// A block of 32 values along a row shares the scale 2^e, one byte e + 127; a
+// value is an E2M1 code, two a byte (OCP Microscaling Formats v1.0, MXFP4).
+// The scale needs no floating-point logarithm: with the absmax's bits b,
+// floor(log2) + 127 is its exponent field b >> 23, so the byte is
+// max((b >> 23) - 2, 0), and 255 exactly where the block holds an infinity or
+// a NaN (their bits are the largest as integers too).  x / 2^e is exact in f32
+// (v_ldexp_f32) and the hardware conversion rounds it to nearest even.
+//
+// All three are bound by memory (and below ~1 MB by the launch): one pass,
+// 16-byte loads, a unit of 512 columns a wave, so that a row's scales leave as
+// 16 bytes a unit.
+#include "../../include/w8a8_experts.h"
+#include "block.hpp"
+#include "internal.hpp"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 512;      // columns of a row that a wave takes at a time: 16 scale bytes
+constexpr int kUnitsInFlight = 4;
+constexpr int kPadByte = 127;   // padding of a row's scales: the scale 1
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The scale byte of a block from its absmax's bits.
+__device__ __forceinline__ int scale_byte(uint32_t amax) {
+    const int exponent = (int)(amax >> 23);
+    return exponent == 255 ? 255 : max(exponent - 2, 0);
+}
+
+// 8 values as 8 codes with the block's scale byte; codes 0 beside a NaN scale.
+__device__ __forceinline__ uint32_t codes_of(const float *v, int byte) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(__builtin_ldexpf(v[i], 127 - byte), -6.0f, 6.0f);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, y[0], y[1], 1.0f, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, y[2], y[3], 1.0f, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, y[4], y[5], 1.0f, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, y[6], y[7], 1.0f, 3);
+    return byte == 255 ? 0u : r;
+}
+
+// 8 consecutive elements of a row as floats, those past K as 0.
+template <class X>
+struct Eight {
+    v4u d[8 / X::kVec];
+    __device__ __forceinline__ void load(const typename X::type *row, int col, int K) {
+#pragma unroll
+        for (int i = 0; i < 8 / X::kVec; ++i) {
+            if (col + i * X::kVec < K) d[i] = load_row_chunk<X>(row, col + i * X::kVec, K);
+            else d[i] = v4u{0u, 0u, 0u, 0u};
+        }
+    }
+    __device__ __forceinline__ void unpack(float *v) const {
+#pragma unroll
+        for (int i = 0; i < 8 / X::kVec; ++i) X::unpack(d[i], v + i * X::kVec);
+    }
+};
+
+// Units of a row: whole ones cover the padded scales too.
+__host__ __device__ inline int64_t units_of(int64_t ldq) { return (ldq + kUnit - 1) / kUnit; }
+
+// A wave takes kUnitsInFlight consecutive units, their loads all in flight
+// before the first is converted.  Lane l holds columns 8 l .. 8 l + 7 of a
+// unit; the four lanes of a block share its absmax.
+template <class X>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const typename X::type *x, int64_t units, int per_row, int K,
+                                                            int64_t ldx, uint8_t *xq, int ldq, uint8_t *xs) {
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = wave * kUnitsInFlight;
+    if (first >= units) return;
+    int64_t row = first / per_row;
+    int unit = (int)(first - row * per_row);
+    Eight<X> in[kUnitsInFlight];
+    {
+        int64_t r = row;
+        int u = unit;
+#pragma unroll
+        for (int i = 0; i < kUnitsInFlight; ++i) {
+            if (first + i < units) in[i].load(x + r * ldx, u * kUnit + lane * 8, K);
+            if (++u == per_row) {
+                u = 0;
+                ++r;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnitsInFlight; ++i) {
+        if (first + i >= units) return;
+        float v[8];
+        in[i].unpack(v);
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = max(amax, abs_bits(v[e]));
+        // quad_perm [1,0,3,2], then [2,3,0,1]: the greatest of the block's four lanes
+        amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, true));
+        amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, true));
+        const int col = unit * kUnit + lane * 8;
+        const int byte = scale_byte(amax);
+        if (col < ldq) *reinterpret_cast<uint32_t *>(xq + row * (ldq / 2) + col / 2) = codes_of(v, byte);
+        if ((lane & 3) == 0) xs[(row * per_row + unit) * 16 + lane / 4] = (uint8_t)(col < ldq ? byte : kPadByte);
+        if (++unit == per_row) {
+            unit = 0;
+            ++row;
+        }
+    }
+}
+
+// Transposed: a workgroup takes kTileN rows of w (columns of the result: 8
+// blocks) by kTileK columns (rows of the result), loads them row by row, turns
+// them in LDS and converts one block of one result row a thread and step.
+constexpr int kTileN = 256, kTileK = 64;
+
+template <class X>
+__global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(const typename X::type *w, int N, int K,
+                                                                       int64_t ldx, uint8_t *wq, int ldq, uint8_t *ws,
+                                                                       int tiles_n, int tiles_k) {
+    typedef typename X::type T;
+    // a row ends 4 bytes past a whole number of bank rounds: writes of 8 rows
+    // and reads of 64 columns both meet every bank
+    constexpr int kPitch = kTileK + 4 / sizeof(T);
+    __shared__ T tile[kTileN * kPitch];
+    const int64_t b = blockIdx.y;
+    const int tk = blockIdx.x % tiles_k, tn = blockIdx.x / tiles_k;
+    const int n0 = tn * kTileN, k0 = tk * kTileK;
+    const T *src = w + b * (int64_t)N * ldx;
+    constexpr int kLanes = kTileK / X::kVec;         // lanes along a row
+    constexpr int kRows = kThreads / kLanes;         // rows a step
+    const int c = threadIdx.x % kLanes * X::kVec, r0 = threadIdx.x / kLanes;
+    v4u d[kTileN / kRows];
+#pragma unroll
+    for (int i = 0; i < kTileN / kRows; ++i) {
+        const int n = n0 + i * kRows + r0;
+        d[i] = v4u{0u, 0u, 0u, 0u};
+        if (n < N && k0 + c < K) d[i] = load_row_chunk<X>(src + n * ldx, k0 + c, K);
+    }
+#pragma unroll
+    for (int i = 0; i < kTileN / kRows; ++i) {
+        T *dst = tile + (i * kRows + r0) * kPitch + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(dst)[e] = d[i][e];
+    }
+    __syncthreads();
+    const int k = threadIdx.x % kTileK;
+    const int64_t row = b * K + k0 + k;
+    const int stride = (int)units_of(ldq) * 16;
+    if (k0 + k >= K) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int nb = threadIdx.x / kTileK + 4 * i;  // block of the tile
+        const int blk = n0 / 32 + nb;                 // block of the row
+        if (blk * 32 >= ldq) {
+            if (blk < stride) ws[row * stride + blk] = (uint8_t)kPadByte;
+            continue;
+        }
+        float v[32];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            v[e] = X::load(tile + (nb * 32 + e) * kPitch + k);
+            amax = max(amax, abs_bits(v[e]));
+        }
+        const int byte = scale_byte(amax);
+        v4u out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = codes_of(v + 8 * e, byte);
+        *reinterpret_cast<v4u *>(wq + row * (ldq / 2) + blk * 16) = out;
+        ws[row * stride + blk] = (uint8_t)byte;
+    }
+}
+
+// 8 codes a lane and step, as quantize_kernel.
+template <class Y>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *xq, const uint8_t *xs, int64_t units,
+                                                              int per_row, int K, int ldq, typename Y::type *y,
+                                                              int64_t ldy) {
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = wave * kUnitsInFlight;
+    if (first >= units) return;
+    int64_t row = first / per_row;
+    int unit = (int)(first - row * per_row);
+    uint32_t codes[kUnitsInFlight];
+    int bytes[kUnitsInFlight];
+    {
+        int64_t r = row;
+        int u = unit;
+#pragma unroll
+        for (int i = 0; i < kUnitsInFlight; ++i) {
+            const int col = u * kUnit + lane * 8;
+            codes[i] = 0;
+            bytes[i] = 0;
+            if (first + i < units && col < K) {
+                codes[i] = *reinterpret_cast<const uint32_t *>(xq + r * (ldq / 2) + col / 2);
+                bytes[i] = xs[(r * per_row + u) * 16 + lane / 4];
+            }
+            if (++u == per_row) {
+                u = 0;
+                ++r;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnitsInFlight; ++i) {
+        if (first + i >= units) return;
+        const int col = unit * kUnit + lane * 8;
+        if (col < K) {
+            typedef float v2f __attribute__((ext_vector_type(2)));
+            const v2f p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[i], 1.0f, 0),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[i], 1.0f, 1),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[i], 1.0f, 2),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[i], 1.0f, 3)};
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = bytes[i] == 255 ? __builtin_nanf("") : __builtin_ldexpf(p[e / 2][e & 1], bytes[i] - 127);
+#pragma unroll
+            for (int e = 0; e < 8; e += Y::kVec)
+                if (col + e < K) store_row_chunk<Y>(y + row * ldy, col + e, K, v + e);
+        }
+        if (++unit == per_row) {
+            unit = 0;
+            ++row;
+        }
+    }
+}
+
+w8a8_status check_rows(int64_t M, int64_t K, int64_t ldx, int64_t ldq) {
+    if (M < 0) return W8A8_ERR_INVALID_ARG;
+    if (M > (1 << 30) || K < 1 || K > (1 << 22) || ldx < K || ldx > (1 << 24)) return W8A8_ERR_SHAPE;
+    if (ldq < K || ldq > (1 << 22) || ldq % 32 != 0) return W8A8_ERR_SHAPE;
+    // one launch: units / 16 workgroups of 256 threads, below 2^32 threads
+    if (M * units_of(ldq) > ((int64_t)1 << 27)) return W8A8_ERR_SHAPE;
+    return W8A8_OK;
+}
+
+unsigned unit_blocks(int64_t units) {
+    constexpr int kPerBlock = kThreads / 64 * kUnitsInFlight;
+    return (unsigned)((units + kPerBlock - 1) / kPerBlock);
+}
+
+}  // namespace
+}  // namespace w8a8
+
+extern "C" int64_t mxfp4_scale_stride(int64_t ldq) { return ldq <= 0 ? 0 : w8a8::units_of(ldq) * 16; }
+
+extern "C" w8a8_status mxfp4_quantize(w8a8_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, uint8_t *xq,
+                                      int64_t ldq, uint8_t *xs, hipStream_t stream) {
+    using namespace w8a8;
+    if (!valid_dtype(xt)) return W8A8_ERR_INVALID_ARG;
+    const w8a8_status st = check_rows(M, K, ldx, ldq);
+    if (st != W8A8_OK) return st;
+    if (M == 0) return W8A8_OK;
+    if (!x || !xq || !xs) return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(xs)) return W8A8_ERR_ALIGN;
+    const int per_row = (int)units_of(ldq);
+    const int64_t units = M * per_row;
+    if (xt == W8A8_BF16)
+        quantize_kernel<Bf16><<<unit_blocks(units), kThreads, 0, stream>>>(static_cast<const uint16_t *>(x), units,
+                                                                           per_row, (int)K, ldx, xq, (int)ldq, xs);
+    else
+        quantize_kernel<F32><<<unit_blocks(units), kThreads, 0, stream>>>(static_cast<const float *>(x), units, per_row,
+                                                                          (int)K, ldx, xq, (int)ldq, xs);
+    return launch_status();
+}
+
+extern "C" w8a8_status mxfp4_quantize_transposed(w8a8_dtype xt, const void *w, int64_t B, int64_t N, int64_t K,
+                                                 int64_t ldx, uint8_t *wq, int64_t ldq, uint8_t *ws,
+                                                 hipStream_t stream) {
+    using namespace w8a8;
+    if (!valid_dtype(xt) || B < 0) return W8A8_ERR_INVALID_ARG;
+    if (B > 65535 || N < 1 || N > (1 << 22) || K < 1 || K > (1 << 22) || ldx < K || ldx > (1 << 24))
+        return W8A8_ERR_SHAPE;
+    if (ldq < N || ldq > (1 << 22) || ldq % 32 != 0) return W8A8_ERR_SHAPE;
+    if (B == 0) return W8A8_OK;
+    if (N * ldx > ((int64_t)1 << 40) / B) return W8A8_ERR_SHAPE;
+    // the tiles that hold the padding of the scales too
+    const int64_t tiles_n = units_of(ldq) * (kUnit / kTileN), tiles_k = (K + kTileK - 1) / kTileK;
+    if (tiles_n * tiles_k * B >= ((int64_t)1 << 24)) return W8A8_ERR_SHAPE;  // 2^32 threads
+    if (!w || !wq || !ws) return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(w) || !aligned16(wq) || !aligned16(ws)) return W8A8_ERR_ALIGN;
+    const dim3 grid((unsigned)(tiles_n * tiles_k), (unsigned)B);
+    if (xt == W8A8_BF16)
+        quantize_transposed_kernel<Bf16><<<grid, kThreads, 0, stream>>>(static_cast<const uint16_t *>(w), (int)N,
+                                                                        (int)K, ldx, wq, (int)ldq, ws, (int)tiles_n,
+                                                                        (int)tiles_k);
+    else
+        quantize_transposed_kernel<F32><<<grid, kThreads, 0, stream>>>(static_cast<const float *>(w), (int)N, (int)K,
+                                                                       ldx, wq, (int)ldq, ws, (int)tiles_n,
+                                                                       (int)tiles_k);
+    return launch_status();
+}
+
+extern "C" w8a8_status mxfp4_dequantize(const uint8_t *xq, const uint8_t *xs, int64_t M, int64_t K, int64_t ldq,
+                                        w8a8_dtype yt, void *y, int64_t ldy, hipStream_t stream) {
+    using namespace w8a8;
+    if (!valid_dtype(yt)) return W8A8_ERR_INVALID_ARG;
+    const w8a8_status st = check_rows(M, K, ldy, ldq);
+    if (st != W8A8_OK) return st;
+    if (M == 0) return W8A8_OK;
+    if (!xq || !xs || !y) return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(xs) || !aligned16(y)) return W8A8_ERR_ALIGN;
+    const int per_row = (int)units_of(ldq);
+    const int64_t units = M * per_row;
+    if (yt == W8A8_BF16)
+        dequantize_kernel<Bf16><<<unit_blocks(units), kThreads, 0, stream>>>(
+            xq, xs, units, per_row, (int)K, (int)ldq, static_cast<uint16_t *>(y), ldy);
+    else
+        dequantize_kernel<F32><<<unit_blocks(units), kThreads, 0, stream>>>(xq, xs, units, per_row, (int)K, (int)ldq,
+                                                                            static_cast<float *>(y), ldy);
+    return launch_status();
+}
