@@ -87,6 +87,7 @@ GROUPS = [
     ([1], 1, 32), ([1], 1024, 1024), ([0, 1, 0], 15, 64), ([3, 0, 1, 5], 40, 96), ([16, 17, 15, 1, 0, 2], 257, 160),
     ([1] * 8, 520, 4096), ([33, 64, 65, 1], 130, 288), ([0, 0, 0], 64, 64), ([200, 0, 3], 100, 544),
     ([2, 300, 61], 264, 1056), ([129] * 3, 256, 256), ([513, 40, 0, 255], 300, 512), ([700], 520, 768),
+    ([1500, 0, 700, 2001], 4100, 96), ([4200], 4104, 544), ([90, 8000], 2056, 256),
 ]
 
 

@@ -143,7 +143,8 @@ def test_round_trip_is_a_projection(w8):
 # ------------------------------------------------------------------ product
 LINEAR = [(1, 1, 32), (1, 1024, 1024), (2, 15, 64), (16, 16, 96), (17, 40, 256), (33, 100, 288), (48, 257, 480),
           (64, 64, 512), (65, 130, 544), (130, 520, 1056), (257, 300, 2080), (300, 264, 160), (520, 1000, 768),
-          (1100, 257, 512)]
+          (1100, 257, 512),
+          (4200, 4100, 32), (4100, 4104, 1056)]
 
 
 def _operand(g, rows, K, lo=120, hi=134):

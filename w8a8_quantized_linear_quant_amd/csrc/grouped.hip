@@ -26,7 +26,12 @@ w8a8_status check(const void *xq, int64_t X, const void *wq, const void *out, co
 template <int QT>
 w8a8_status launch_grouped(const GroupedArgs &a, hipStream_t stream) {
     if (a.M == 0 || a.N == 0) return W8A8_OK;
-    launch_grouped_rows<QT>(a, stream);
+    if (a.M > 64 * (int64_t)a.E) {
+        const int64_t tiles = ((a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
+        launch_grouped_tiles<QT>(a, tiles >= device_cu_count() ? 256 : 128, stream);
+    } else {
+        launch_grouped_rows<QT>(a, stream);
+    }
     return launch_status();
 }
 

@@ -110,6 +110,6 @@ template <int QT>
 void launch_grouped_rows(const GroupedArgs &a, hipStream_t stream);
 // grouped_tiles.hip: many rows a group.
 template <int QT>
-void launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream);
+void launch_grouped_tiles(const GroupedArgs &a, int edge, hipStream_t stream);
 
 }  // namespace w8a8

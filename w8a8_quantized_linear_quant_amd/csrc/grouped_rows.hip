@@ -196,8 +196,7 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
             const size_t at = (size_t)t.group * p.N + n + i;
             const float bias = p.bias ? bf16_bits_to_f32(p.bias[at]) : 0.0f;
             if constexpr (kMx) y[i] = s[i] + bias;
-            else if (p.per_channel) y[i] = (float)s[i] * tm * p.sw[at] + bias;
-            else y[i] = __builtin_fmaf((float)s[i], tm, bias);
+            else y[i] = __builtin_fmaf((float)s[i], p.per_channel ? tm * p.sw[at] : tm, bias);
         }
         uint16_t *dst = p.out + (size_t)m * p.N + n;
         if ((p.N & 3) == 0) {
