@@ -361,12 +361,17 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                  asm volatile("" : "+v"(o0), "+v"(o1));
                  const uint8_t *src = kLast ? nxt : cur;
                  const uint8_t *lp0 = src + o0, *lp1 = src + o1;
-                 int so = frow * 16 + (S == 0 ? 8 : 0) + fq * 4;
-                 asm volatile("" : "+v"(so));
-                 const uint8_t *sp = (S == 0 ? slab_cur : slab_next) + so;
+                 if constexpr (kMx && kLast) {
+                     // the next stage's scale words.  Before this step's loads: which buffer they are in is not
+                     // known when compiling, so each read waits for the loads in flight -- there are none here.
+                     const uint8_t *sp = (S == 0 ? slab_cur : slab_next) + frow * 16 + (S == 0 ? 8 : 0) + fq * 4;
+                     [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
+                         (read_scale(sp, std::integral_constant<int, R>{}, sa[1 - S], sb[1 - S]), ...);
+                     }(std::make_integer_sequence<int, 2 * kNB>{});
+                     __builtin_amdgcn_sched_barrier(0);
+                 }
                  constexpr int kPer = kInt8 ? 4 : 1;                // products of a group
                  constexpr int kGroups = kNB * kNB / kPer;
-                 constexpr int kR = kReads + (kMx && kLast ? 2 * kNB : 0);
                  constexpr int kL = kLast ? kLoads : 0;
                  [&]<int... G>(std::integer_sequence<int, G...>) __attribute__((always_inline)) {
                      (([&]() __attribute__((always_inline)) {
@@ -380,12 +385,11 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                           }(std::make_integer_sequence<int, kPer>{});
                           [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
                               (([&]() __attribute__((always_inline)) {
-                                   constexpr int r = share_first(g, kR, kGroups) + R;
-                                   if constexpr (r < kReads) read_one(lp0, lp1, std::integral_constant<int, r>{}, fa[P ^ 1], fb[P ^ 1]);
-                                   else read_scale(sp, std::integral_constant<int, r - kReads>{}, sa[1 - S], sb[1 - S]);
+                                   constexpr int r = share_first(g, kReads, kGroups) + R;
+                                   read_one(lp0, lp1, std::integral_constant<int, r>{}, fa[P ^ 1], fb[P ^ 1]);
                                }()),
                                ...);
-                          }(std::make_integer_sequence<int, share_count(g, kR, kGroups)>{});
+                          }(std::make_integer_sequence<int, share_count(g, kReads, kGroups)>{});
                           [&]<int... L>(std::integer_sequence<int, L...>) __attribute__((always_inline)) {
                               (load_one(cur, std::integral_constant<int, share_first(g, kL, kGroups) + L>{}), ...);
                           }(std::make_integer_sequence<int, share_count(g, kL, kGroups)>{});
@@ -417,23 +421,23 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
     asm volatile("s_barrier" ::: "memory");
 
     uint8_t *slab_cur = slab0, *slab_next = slab1;
+    // the first step's fragments; a tile's last step reads the next tile's
+    {
+        int o0 = foff(0, 0), o1 = foff(0, kRegs - 1), so = frow * 16 + fq * 4;
+        asm volatile("" : "+v"(o0), "+v"(o1), "+v"(so));
+        [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
+            (read_one(lds0 + o0, lds0 + o1, std::integral_constant<int, R>{}, fa[0], fb[0]), ...);
+        }(std::make_integer_sequence<int, kReads>{});
+        if constexpr (kMx) {
+            [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
+                (read_scale(slab_cur + so, std::integral_constant<int, R>{}, sa[0], sb[0]), ...);
+            }(std::make_integer_sequence<int, 2 * kNB>{});
+        }
+    }
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         // the cursor is two stages on: in this tile, or past it if it has no more
         const Tile c = stages == 2 ? before : loading;
         const int mw = c.m0 + wm * WT, nw = c.n0 + wn * WT;
-        // stage 0 has landed (prologue, or the previous tile's last stage waited for it)
-        {
-            int o0 = foff(0, 0), o1 = foff(0, kRegs - 1), so = frow * 16 + fq * 4;
-            asm volatile("" : "+v"(o0), "+v"(o1), "+v"(so));
-            [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
-                (read_one(lds0 + o0, lds0 + o1, std::integral_constant<int, R>{}, fa[0], fb[0]), ...);
-            }(std::make_integer_sequence<int, kReads>{});
-            if constexpr (kMx) {
-                [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
-                    (read_scale(slab_cur + so, std::integral_constant<int, R>{}, sa[0], sb[0]), ...);
-                }(std::make_integer_sequence<int, 2 * kNB>{});
-            }
-        }
         // Inputs of the epilogue, one or two rows and columns a lane: the rows' indices now, what they point to two
         // stages before the end, so that nothing waits for memory in between.
         constexpr int kPart = WT / 64;
@@ -529,7 +533,18 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
         constexpr int kCB = kPassCols / kBlk, kRB = 32 / kBlk;  // blocks of a pass
         constexpr int kOutChunks = kPassCols / 8, kOutRows = 64 / kOutChunks;
 #pragma unroll
-        for (int cp = 0; cp < WT / kPassCols; ++cp)
+        for (int cp = 0; cp < WT / kPassCols; ++cp) {
+            v4f bias[kMx ? 1 : kCB][kMx ? 1 : kQuads], channel[kMx ? 1 : kCB][kMx ? 1 : kQuads];
+            if constexpr (!kMx) {
+#pragma unroll
+                for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+                    for (int q = 0; q < kQuads; ++q) {
+                        const float *at = ep + WT + (cp * kCB + cb) * kBlk + 8 * q + cq;
+                        bias[cb][q] = *reinterpret_cast<const v4f *>(at);
+                        channel[cb][q] = *reinterpret_cast<const v4f *>(at + WT);
+                    }
+            }
 #pragma unroll
             for (int ps = 0; ps < WT / 32; ++ps) {
                 __builtin_amdgcn_sched_barrier(0);  // one pass's accumulators in ordinary registers at a time
@@ -551,10 +566,9 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                                 y[2] = v[2] + bf16_bits_to_f32(b.y & 0xFFFFu);
                                 y[3] = v[3] + bf16_bits_to_f32(b.y >> 16);
                             } else {
-                                const v4f b = *reinterpret_cast<const v4f *>(ep + WT + nb * kBlk + 8 * q + cq);
-                                const v4f ch = *reinterpret_cast<const v4f *>(ep + 2 * WT + nb * kBlk + 8 * q + cq);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(v[i], tm[mb] * ch[i], b[i]);
+                                for (int i = 0; i < 4; ++i)
+                                    y[i] = __builtin_fmaf(v[i], tm[mb] * channel[cb][q][i], bias[cb][q][i]);
                             }
                             const int row = rb * kBlk + brow, col = cb * kBlk + 8 * q + cq;
                             const int chunk = (col >> 3) ^ (row & (kOutChunks - 1));
@@ -571,7 +585,9 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                     if (m >= c.end) continue;
                     uint16_t *dst = p.out + (size_t)m * N + n;
                     if ((N & 7) == 0) {
-                        if (n < N) *reinterpret_cast<v4u *>(dst) = d;
+                        // whole 128-byte lines past the caches; parts of lines through them, to be merged there
+                        if (n < N && (N & 63) == 0) __builtin_nontemporal_store(d, reinterpret_cast<v4u *>(dst));
+                        else if (n < N) *reinterpret_cast<v4u *>(dst) = d;
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -580,6 +596,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                 }
                 __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
             }
+        }
     }
     // loads for stages past the last tile may still be in flight
     __builtin_amdgcn_s_waitcnt(kWaitVm0);
