@@ -28,7 +28,7 @@ w8a8_status launch_grouped(const GroupedArgs &a, hipStream_t stream) {
     if (a.M == 0 || a.N == 0) return W8A8_OK;
     if (a.M > 64 * (int64_t)a.E) {
         const int64_t tiles = ((a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
-        launch_grouped_tiles<QT>(a, tiles >= device_cu_count() ? 256 : 128, stream);
+        launch_grouped_tiles<QT>(a, tiles >= device_cu_count() ? kTile256 : kTile128Deep, stream);
     } else {
         launch_grouped_rows<QT>(a, stream);
     }

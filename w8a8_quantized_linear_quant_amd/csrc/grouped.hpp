@@ -109,7 +109,12 @@ __device__ __forceinline__ GroupTile find_tile(GroupWindow &w, int tile, const i
 template <int QT>
 void launch_grouped_rows(const GroupedArgs &a, hipStream_t stream);
 // grouped_tiles.hip: many rows a group.
+enum TileKind {
+    kTile256,      // 256 x 256, a ring of two stages, one workgroup a CU
+    kTile128,      // 128 x 128, a ring of two, two workgroups a CU
+    kTile128Deep,  // 128 x 128, a ring of four, one workgroup a CU
+};
 template <int QT>
-void launch_grouped_tiles(const GroupedArgs &a, int edge, hipStream_t stream);
+void launch_grouped_tiles(const GroupedArgs &a, TileKind kind, hipStream_t stream);
 
 }  // namespace w8a8

@@ -41,8 +41,10 @@ constexpr int kTilesTogether = 4;  // row tiles that advance together along N
 
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
-constexpr int kWaitVm0 = (7 << 4) | (15 << 8);                // vmcnt(0)
-constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);         // lgkmcnt(0)
+// s_waitcnt: at most n vector memory operations in flight; no LDS operation
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+constexpr int kWaitVm0 = wait_vm(0);
+constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);
 
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 constexpr int share_first(int g, int total, int groups) { return g * total / groups; }
@@ -83,8 +85,8 @@ __device__ __forceinline__ int load_i32(__amdgpu_buffer_rsrc_t r, int off) {
     return (int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
 
-template <int QT, int WT, bool TAIL>
-__global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kernel(GroupedArgs p, int tiles_n) {
+template <int QT, int WT, int NST, bool TAIL>
+__global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void grouped_tiles_kernel(GroupedArgs p, int tiles_n) {
     constexpr bool kInt8 = QT == kTypeInt8, kMx = QT == kTypeMx4;
     constexpr int BT = 2 * WT;                      // tile edge
     constexpr int kOpBytes = BT * kStageK;          // one operand's stage
@@ -97,6 +99,8 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
     constexpr int kPassBytes = 32 * kPassCols * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kOpBytes];
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[2 * kOpBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds2[NST == 4 ? 2 * kOpBytes : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds3[NST == 4 ? 2 * kOpBytes : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t slab0[kMx ? kSlabBytes : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t slab1[kMx ? kSlabBytes : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t obuf[4 * kPassBytes];
@@ -108,8 +112,9 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
     const int wm = wave >> 1, wn = wave & 1;
     const int kb = p.kb, M = p.M, N = p.N;
     const bool gather = p.rows != nullptr;
-    // stages of a tile: an even number, so that every tile starts in the same buffer (those past K read zeros)
-    const int stages = (kb + 2 * kStageK - 1) / (2 * kStageK) * 2;
+    static_assert(NST == 2 || NST == 4, "stages in the ring");
+    // stages of a tile: whole turns of the ring, so that every tile starts in the same buffer (those past K read zeros)
+    const int stages = (kb + NST * kStageK - 1) / (NST * kStageK) * NST;
 
     GroupWindow win = {};
     load_window<BT>(win, p.offsets, p.E, M, lane);
@@ -322,25 +327,41 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
         }
 #endif
     };
-    auto buffer = [&](auto s) -> uint8_t * { return decltype(s)::value ? lds1 : lds0; };
+    auto buffer = [&](auto s) __attribute__((always_inline)) -> uint8_t * {
+        constexpr int S = decltype(s)::value;
+        if constexpr (S == 0) return lds0;
+        else if constexpr (S == 1) return lds1;
+        else if constexpr (S == 2) return lds2;
+        else return lds3;
+    };
 
-    // Stage S (0 or 1) of a pair; `slab_cur` holds the pair's scales and
-    // `slab_next` the next pair's.  While a step is multiplied, the next one's
-    // fragments are read.  Before the stage's last step: everything in flight
-    // has landed (the next stage), every wave has read the last of this one;
-    // then this buffer takes the stage two ahead.
+    // Stage S of a turn.  While a step is multiplied, the next one's fragments
+    // are read.  Before the stage's last step: the next stage has landed, and
+    // every wave has read the last of this one (barrier).  Loads: with two
+    // stages this buffer takes the stage two ahead, in its last step; with four
+    // the buffer of the stage before takes the stage three ahead, in every step.
+    // Scales.  Two stages: slab_cur holds this turn's, slab_next the next one's,
+    // and they change places.  Four: slab0 holds those of stages 0 and 1, slab1
+    // of 2 and 3, each loaded again for the next turn after the stage (1, 3)
+    // during whose last step no wave reads it any more.
+    constexpr int kPart = NST == 2 ? kLoads : kLoads / KSTEPS;  // loads of a step that has any
+    // loads in flight that may be newer than the next stage's
+    constexpr int kNewer = NST == 2 ? 0 : kLoads + (KSTEPS - 1) * kPart;
+    static_assert(kLoads % KSTEPS == 0, "loads split evenly over a stage's steps");
     auto run_stage = [&](auto sc, auto first_c, const uint8_t *slab_cur, uint8_t *slab_next, int kt) __attribute__((always_inline)) {
         constexpr int S = decltype(sc)::value;
         constexpr bool FIRST = decltype(first_c)::value;
-        uint8_t *cur = buffer(sc), *nxt = buffer(std::integral_constant<int, 1 - S>{});
+        uint8_t *cur = buffer(sc), *nxt = buffer(std::integral_constant<int, (S + 1) % NST>{});
+        uint8_t *refill = NST == 2 ? cur : buffer(std::integral_constant<int, (S + 3) % NST>{});
+        constexpr int Q = S & 1;  // which of the two sets of scale words
         if constexpr (kMx && TAIL) {
             // bytes past the row's scales count as 2^-127 (their codes are 0, but 0 times NaN is not)
             const int have = min(max(kb / 16 - kt * 8 - fq * 4, 0), 4);
             const int keep = have == 4 ? -1 : (1 << (8 * have)) - 1;
 #pragma unroll
             for (int b = 0; b < kNB; ++b) {
-                sa[S][b] &= keep;
-                sb[S][b] &= keep;
+                sa[Q][b] &= keep;
+                sb[Q][b] &= keep;
             }
             asm volatile("s_nop 4" ::: "memory");  // the products are assembly: their wait for these words is this one
         }
@@ -349,7 +370,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                  constexpr int kk = KK, P = kk & 1;
                  constexpr bool kLast = kk + 1 == KSTEPS;
                  if constexpr (kLast) {
-                     __builtin_amdgcn_s_waitcnt(kWaitVm0);
+                     __builtin_amdgcn_s_waitcnt(wait_vm(kNewer));
                      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
                      // a bare barrier: __syncthreads() would also wait for what was issued for later stages
                      asm volatile("s_barrier" ::: "memory");
@@ -362,25 +383,28 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                  const uint8_t *src = kLast ? nxt : cur;
                  const uint8_t *lp0 = src + o0, *lp1 = src + o1;
                  if constexpr (kMx && kLast) {
-                     // the next stage's scale words.  Before this step's loads: which buffer they are in is not
-                     // known when compiling, so each read waits for the loads in flight -- there are none here.
-                     const uint8_t *sp = (S == 0 ? slab_cur : slab_next) + frow * 16 + (S == 0 ? 8 : 0) + fq * 4;
+                     // The next stage's scale words.  Two stages: before this step's loads -- which buffer they are in
+                     // is not known when compiling, so each read waits for the loads in flight; there are none here.
+                     constexpr int n = (S + 1) % NST;
+                     const uint8_t *slab = NST == 4 ? (n < 2 ? slab0 : slab1) : S == 0 ? slab_cur : slab_next;
+                     int so = frow * 16 + (n & 1) * 8 + fq * 4;
+                     asm volatile("" : "+v"(so));
                      [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
-                         (read_scale(sp, std::integral_constant<int, R>{}, sa[1 - S], sb[1 - S]), ...);
+                         (read_scale(slab + so, std::integral_constant<int, R>{}, sa[1 - Q], sb[1 - Q]), ...);
                      }(std::make_integer_sequence<int, 2 * kNB>{});
                      __builtin_amdgcn_sched_barrier(0);
                  }
                  constexpr int kPer = kInt8 ? 4 : 1;                // products of a group
                  constexpr int kGroups = kNB * kNB / kPer;
-                 constexpr int kL = kLast ? kLoads : 0;
+                 constexpr int kL = NST == 4 ? kPart : kLast ? kLoads : 0, kL0 = NST == 4 ? kk * kPart : 0;
                  [&]<int... G>(std::integer_sequence<int, G...>) __attribute__((always_inline)) {
                      (([&]() __attribute__((always_inline)) {
                           constexpr int g = G;
                           constexpr auto first = std::integral_constant<bool, FIRST && S == 0 && kk == 0>{};
                           [&]<int... J>(std::integer_sequence<int, J...>) __attribute__((always_inline)) {
                               (product(acc[(g * kPer + J) / kNB][(g * kPer + J) % kNB], fa[P][(g * kPer + J) / kNB],
-                                       fb[P][(g * kPer + J) % kNB], sa[S][kMx ? (g * kPer + J) / kNB : 0],
-                                       sb[S][kMx ? (g * kPer + J) % kNB : 0], std::integral_constant<int, kk>{}, first),
+                                       fb[P][(g * kPer + J) % kNB], sa[Q][kMx ? (g * kPer + J) / kNB : 0],
+                                       sb[Q][kMx ? (g * kPer + J) % kNB : 0], std::integral_constant<int, kk>{}, first),
                                ...);
                           }(std::make_integer_sequence<int, kPer>{});
                           [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
@@ -391,7 +415,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                                ...);
                           }(std::make_integer_sequence<int, share_count(g, kReads, kGroups)>{});
                           [&]<int... L>(std::integer_sequence<int, L...>) __attribute__((always_inline)) {
-                              (load_one(cur, std::integral_constant<int, share_first(g, kL, kGroups) + L>{}), ...);
+                              (load_one(refill, std::integral_constant<int, kL0 + share_first(g, kL, kGroups) + L>{}), ...);
                           }(std::make_integer_sequence<int, share_count(g, kL, kGroups)>{});
                           __builtin_amdgcn_sched_barrier(0);
                       }()),
@@ -400,6 +424,8 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
              }()),
              ...);
         }(std::make_integer_sequence<int, KSTEPS>{});
+        if constexpr (NST == 4 && S == 1) load_slab(slab0);
+        if constexpr (NST == 4 && S == 3) load_slab(slab1);
         advance();
     };
 
@@ -412,12 +438,23 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
         enter_tile(c, lr, sr);
         look_ahead();
     }
+    auto load_stage = [&](uint8_t *stage) __attribute__((always_inline)) {
+        [&]<int... J>(std::integer_sequence<int, J...>) __attribute__((always_inline)) {
+            (load_one(stage, std::integral_constant<int, J>{}), ...);
+        }(std::make_integer_sequence<int, kLoads>{});
+        advance();
+    };
     load_slab(slab0);
-    [&]<int... J>(std::integer_sequence<int, J...>) __attribute__((always_inline)) { (load_one(lds0, std::integral_constant<int, J>{}), ...); }(std::make_integer_sequence<int, kLoads>{});
-    advance();
-    [&]<int... J>(std::integer_sequence<int, J...>) __attribute__((always_inline)) { (load_one(lds1, std::integral_constant<int, J>{}), ...); }(std::make_integer_sequence<int, kLoads>{});
-    advance();
-    __builtin_amdgcn_s_waitcnt(kWaitVm0);
+    load_stage(lds0);
+    load_stage(lds1);
+    if constexpr (NST == 4) {
+        load_slab(slab1);
+        load_stage(lds2);
+        // stages 1 and 2 and the second scales may be in flight
+        __builtin_amdgcn_s_waitcnt(wait_vm(2 * kLoads + (kMx ? kSlabLoads : 0)));
+    } else {
+        __builtin_amdgcn_s_waitcnt(kWaitVm0);
+    }
     asm volatile("s_barrier" ::: "memory");
 
     uint8_t *slab_cur = slab0, *slab_next = slab1;
@@ -430,26 +467,26 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
         }(std::make_integer_sequence<int, kReads>{});
         if constexpr (kMx) {
             [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
-                (read_scale(slab_cur + so, std::integral_constant<int, R>{}, sa[0], sb[0]), ...);
+                (read_scale(slab0 + so, std::integral_constant<int, R>{}, sa[0], sb[0]), ...);
             }(std::make_integer_sequence<int, 2 * kNB>{});
         }
     }
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        // the cursor is two stages on: in this tile, or past it if it has no more
-        const Tile c = stages == 2 ? before : loading;
+        // the cursor is two stages on (three in a ring of four): in this tile, or past it if it has no more
+        const Tile c = NST == 2 && stages == 2 ? before : loading;
         const int mw = c.m0 + wm * WT, nw = c.n0 + wn * WT;
         // Inputs of the epilogue, one or two rows and columns a lane: the rows' indices now, what they point to two
         // stages before the end, so that nothing waits for memory in between.
-        constexpr int kPart = WT / 64;
-        int erow[kMx ? 1 : kPart];
-        float escale[kMx ? 1 : kPart], echannel[kMx ? 1 : kPart];
-        uint16_t ebias[kPart];
+        constexpr int kSets = WT / 64;
+        int erow[kMx ? 1 : kSets];
+        float escale[kMx ? 1 : kSets], echannel[kMx ? 1 : kSets];
+        uint16_t ebias[kSets];
         const size_t col0 = (size_t)c.group * N;
         float tensor_scale = 1.0f;
         if constexpr (!kMx) {
             const __amdgpu_buffer_rsrc_t r = small_rsrc(p.rows + mw, gather ? some(c.end - mw, WT) * 4 : 0);
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) {
+            for (int i = 0; i < kSets; ++i) {
                 const int m = i * 64 + lane;
                 const int v = load_i32(r, m * 4);
                 erow[i] = mw + m >= c.end ? -1 : gather ? v : m;
@@ -459,7 +496,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
             const int cols = some(N - nw, WT);
             const __amdgpu_buffer_rsrc_t rb = small_rsrc(p.bias + col0 + nw, p.bias ? cols * 2 : 0);
 #pragma unroll
-            for (int i = 0; i < kPart; ++i)
+            for (int i = 0; i < kSets; ++i)
                 ebias[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, (i * 64 + lane) * 2, 0, 0);
             if constexpr (!kMx) {
                 // rows of x: all of it where they are gathered, the tile's own otherwise
@@ -467,7 +504,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                     small_rsrc(p.sx + (gather ? 0 : mw), gather ? (int)p.X * 4 : some(c.end - mw, WT) * 4);
                 const __amdgpu_buffer_rsrc_t rc = small_rsrc(p.sw + col0 + nw, p.per_channel ? cols * 4 : 0);
 #pragma unroll
-                for (int i = 0; i < kPart; ++i) {
+                for (int i = 0; i < kSets; ++i) {
                     const int off = erow[i] < 0 || erow[i] >= p.X ? kOobOffset : erow[i] * 4;
                     escale[i] = __int_as_float(load_i32(rs, off));
                     const float ch = __int_as_float(load_i32(rc, (i * 64 + lane) * 4));
@@ -476,19 +513,20 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
                 tensor_scale = p.per_channel ? 1.0f : p.sw[c.group];
             }
         };
-        auto run_pair = [&](auto first, int kt) __attribute__((always_inline)) {
-            load_slab(slab_next);  // the next pair's scales: the cursor stands at its first stage
-            run_stage(std::integral_constant<int, 0>{}, first, slab_cur, slab_next, kt);
-            run_stage(std::integral_constant<int, 1>{}, std::false_type{}, slab_cur, slab_next, kt + 1);
+        auto run_turn = [&](auto first, int kt) __attribute__((always_inline)) {
+            if constexpr (NST == 2) load_slab(slab_next);  // the next turn's scales: the cursor stands at its first stage
+            [&]<int... S>(std::integer_sequence<int, S...>) __attribute__((always_inline)) {
+                (run_stage(std::integral_constant<int, S>{}, first, slab_cur, slab_next, kt + S), ...);
+            }(std::make_integer_sequence<int, NST>{});
             uint8_t *s = slab_cur;
             slab_cur = slab_next;
             slab_next = s;
         };
-        run_pair(std::true_type{}, 0);
-        if (stages == 2) fetch();
-        for (int kt = 2; kt < stages; kt += 2) {
-            if (kt + 2 == stages) fetch();
-            run_pair(std::false_type{}, kt);
+        run_turn(std::true_type{}, 0);
+        if (stages == NST) fetch();
+        for (int kt = NST; kt < stages; kt += NST) {
+            if (kt + NST == stages) fetch();
+            run_turn(std::false_type{}, kt);
         }
 
         // ---- epilogue: y = bf16(acc * (sx * sw) + bias) through LDS, 32 rows by kPassCols columns at a time
@@ -504,7 +542,7 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
         // where they are used.  4-bit format: the biases alone, as bf16, in the staging area, read beforehand.
         float *ep = reinterpret_cast<float *>(epbuf + wave * kEpBytes);  // [WT] row scales, [WT] biases, [WT] channel scales
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) {
+        for (int i = 0; i < kSets; ++i) {
             if constexpr (kMx) {
                 reinterpret_cast<uint16_t *>(ob)[i * 64 + el] = ebias[i];
             } else {
@@ -602,27 +640,28 @@ __global__ __launch_bounds__(kThreads, WT == 64 ? 2 : 1) void grouped_tiles_kern
     __builtin_amdgcn_s_waitcnt(kWaitVm0);
 }
 
-template <int QT, int WT>
+template <int QT, int WT, int NST>
 void launch(const GroupedArgs &a, hipStream_t stream) {
     constexpr int BT = 2 * WT;
     const int tiles_n = (a.N + BT - 1) / BT;
     // every group may leave one tile partly filled
     const int64_t most = (a.M / BT + (int64_t)(a.E < a.M ? a.E : a.M)) * tiles_n;
-    const int64_t slots = (int64_t)device_cu_count() * (WT == 64 ? 2 : 1);
+    const int64_t slots = (int64_t)device_cu_count() * (WT == 64 && NST == 2 ? 2 : 1);
     const unsigned grid = (unsigned)(most < slots ? most : slots);
-    if (a.kb % (2 * kStageK) == 0) grouped_tiles_kernel<QT, WT, false><<<grid, kThreads, 0, stream>>>(a, tiles_n);
-    else grouped_tiles_kernel<QT, WT, true><<<grid, kThreads, 0, stream>>>(a, tiles_n);
+    if (a.kb % (NST * kStageK) == 0) grouped_tiles_kernel<QT, WT, NST, false><<<grid, kThreads, 0, stream>>>(a, tiles_n);
+    else grouped_tiles_kernel<QT, WT, NST, true><<<grid, kThreads, 0, stream>>>(a, tiles_n);
 }
 
 }  // namespace
 
 template <int QT>
-void launch_grouped_tiles(const GroupedArgs &a, int edge, hipStream_t stream) {
-    if (edge == 256) launch<QT, 128>(a, stream);
-    else launch<QT, 64>(a, stream);
+void launch_grouped_tiles(const GroupedArgs &a, TileKind kind, hipStream_t stream) {
+    if (kind == kTile256) launch<QT, 128, 2>(a, stream);
+    else if (kind == kTile128) launch<QT, 64, 2>(a, stream);
+    else launch<QT, 64, 4>(a, stream);
 }
-template void launch_grouped_tiles<kTypeInt8>(const GroupedArgs &, int, hipStream_t);
-template void launch_grouped_tiles<kTypeE4m3>(const GroupedArgs &, int, hipStream_t);
-template void launch_grouped_tiles<kTypeMx4>(const GroupedArgs &, int, hipStream_t);
+template void launch_grouped_tiles<kTypeInt8>(const GroupedArgs &, TileKind, hipStream_t);
+template void launch_grouped_tiles<kTypeE4m3>(const GroupedArgs &, TileKind, hipStream_t);
+template void launch_grouped_tiles<kTypeMx4>(const GroupedArgs &, TileKind, hipStream_t);
 
 }  // namespace w8a8
