@@ -45,7 +45,7 @@ int64_t mxfp4_scale_stride(int64_t ldq);
  * Quantizes the rows of x [M, ldx] (first K columns, type xt), blocks along K.
  * Columns K .. ldq - 1 of the codes are written as 0.
  * Shape rules: 0 <= M <= 2^30; 1 <= K <= 2^22; K <= ldx <= 2^24, any alignment
- * of the rows; K <= ldq <= 2^22, ldq % 32 == 0.
+ * of the rows; K <= ldq <= 2^22, ldq % 32 == 0; M * ceil(ldq / 512) <= 2^27.
  */
 w8a8_status mxfp4_quantize(w8a8_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, uint8_t *xq, int64_t ldq,
                            uint8_t *xs, hipStream_t stream);
@@ -56,7 +56,8 @@ w8a8_status mxfp4_quantize(w8a8_dtype xt, const void *x, int64_t M, int64_t K, i
  * [B, K, mxfp4_scale_stride(ldq)] of the K rows of N values each, blocks along
  * N.  What the input gradient's product takes as its weight.
  * Shape rules: 0 <= B <= 65535; 1 <= N, K <= 2^22; K <= ldx <= 2^24;
- * N <= ldq <= 2^22, ldq % 32 == 0; B * N * ldx <= 2^40.
+ * N <= ldq <= 2^22, ldq % 32 == 0; B * N * ldx <= 2^40; fewer than 2^24 tiles
+ * of 256 x 64: B * 2 ceil(ldq / 512) * ceil(K / 64).
  */
 w8a8_status mxfp4_quantize_transposed(w8a8_dtype xt, const void *w, int64_t B, int64_t N, int64_t K, int64_t ldx,
                                       uint8_t *wq, int64_t ldq, uint8_t *ws, hipStream_t stream);
@@ -134,6 +135,16 @@ w8a8_status mxfp4_linear_grouped(const uint8_t *xq, int64_t X, const uint8_t *xs
 w8a8_status mxfp4_linear_grouped_backward_dx(const uint8_t *dyq, const uint8_t *dys, const uint8_t *wq_t,
                                              const uint8_t *ws_t, const int32_t *offsets, int64_t E, int64_t M,
                                              int64_t N, int64_t K, uint16_t *dx, hipStream_t stream);
+
+/*
+ * Diagnostic: which kernel a product of M rows in E groups takes on the current
+ * device (type 0 int8, 1 e4m3, 2 the 4-bit format; E = 1 for mxfp4_linear), so
+ * that a test can tell what a shape exercises: 0 .. 3 tiles of 16 x 16, 16 x
+ * 32, 32 x 32, 64 x 64 with operands staged by each wave; 4 and 5 128 x 128
+ * with a ring of four and of two stages; 6 256 x 256.  -1 for sizes below 1 or
+ * another type.  Enqueues nothing.
+ */
+int w8a8_probe_grouped_kernel(int type, int64_t M, int64_t N, int64_t K, int64_t E);
 
 #ifdef __cplusplus
 }

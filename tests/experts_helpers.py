@@ -129,3 +129,31 @@ def assert_close(got, ref, mass, K, exact_sums=False, peak=None, what=""):
     off = (got.double() - ref).abs()
     bad = ~(off <= bound)
     assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), float((off - bound).max()))
+
+
+# (type, kernel of probe_grouped_kernel, M, E, N, K): every kernel, each with a K
+# that fills its ring of stages (the last of a pair) and one that ends inside
+KERNELS = []
+for _kernel, _M, _E, _N, _K8, _K4 in (
+        (0, 37, 3, 100, (160, 512), (160, 1024)), (1, 20, 3, 8200, (160, 512), (1056, 2048)),
+        (2, 700, 9, 516, (160, 512), (544, 1024)), (3, 700, 9, 1000, (2080, 2048), (2080, 2048)),
+        (4, 20, 9, 4100, (288, 512), (288, 1024)),
+        (4, 500, 1, 4100, (2080, 2048), (2080, 4096)), (5, 1400, 1, 4100, (1056, 1024), (2080, 2048)), (5, 100, 9, 4100, (160, 512), (160, 1024)),
+        (6, 4000, 9, 2000, (160, 512), (160, 1024)),
+        (6, 6000, 1, 4100, (1056, 1024), (2080, 2048))):
+    for _type in ("int8", "e4m3", "mx"):
+        for _K in _K4 if _type == "mx" else _K8:
+            KERNELS.append((_type, _kernel, _M, _E, _N, _K))
+
+
+def uneven(M, E):
+    """Lengths of E groups, M in all: one empty, one of a single row where there are enough."""
+    out = [M // E] * E
+    out[-1] += M - sum(out)
+    if E > 2:
+        out[0] += out[1]
+        out[1] = 0
+    if E > 4:
+        out[2] += out[3] - 1
+        out[3] = 1
+    return out

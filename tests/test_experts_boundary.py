@@ -3,6 +3,7 @@ refusals before anything is launched."""
 import pytest
 import torch
 
+import experts_helpers as ref
 import w8a8_quantized_linear_quant_amd as w8
 
 lib = w8.library()
@@ -16,7 +17,8 @@ def test_exports_match_header():
     names = w8.exported_names_in_header(w8.EXPERTS_HEADER)
     assert names == ["mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_backward_dx", "mxfp4_linear_grouped",
                      "mxfp4_linear_grouped_backward_dx", "mxfp4_quantize", "mxfp4_quantize_transposed",
-                     "mxfp4_scale_stride", "w8a8_linear_grouped", "w8a8_linear_grouped_backward_dx"]
+                     "mxfp4_scale_stride", "w8a8_linear_grouped", "w8a8_linear_grouped_backward_dx",
+                     "w8a8_probe_grouped_kernel"]
     for n in names:
         assert hasattr(lib, n), n
 
@@ -146,3 +148,15 @@ def test_binding_wants_gpu_tensors():
         w8.w8a8_linear_grouped(u8, None, u8[None], None, None)
     with pytest.raises(ValueError, match="w_scale must be"):
         w8.w8a8_linear_grouped_backward_dx(i8, None, i8[None], torch.zeros(1, 4), None)
+
+
+def test_the_kernels_that_the_gpu_tests_name():
+    for kind, kernel, M, E, N, K in ref.KERNELS:
+        assert w8.probe_grouped_kernel(kind, M, N, K, E) == kernel, (kind, kernel, M, E, N, K)
+    assert {k[:2] for k in ref.KERNELS} == {(t, k) for t in ("int8", "e4m3", "mx") for k in range(7)}
+
+
+def test_probe_rejects():
+    for args in ((0, 0, 8, 64, 1), (0, 8, 0, 64, 1), (0, 8, 8, 0, 1), (0, 8, 8, 64, 0), (3, 8, 8, 64, 1), (-1, 8, 8, 64, 1),
+                 (0, 8, 8, 64, 4097), (2, (1 << 30) + 1, 8, 64, 1)):
+        assert lib.w8a8_probe_grouped_kernel(*args) == -1, args

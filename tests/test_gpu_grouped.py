@@ -122,6 +122,23 @@ def test_whole_numbers_are_exact(w8, kind, lengths, N, K):
     c.check(w8, _offsets(lengths), M, rows=_rows(M, M, N), exact=True)
 
 
+@pytest.mark.parametrize("kind,kernel,M,E,N,K", ref.KERNELS)
+def test_every_kernel(w8, kind, kernel, M, E, N, K):
+    """Each kernel with whole numbers, exactly, and with random ones; rows in
+    order and gathered, rows in no group, a bias, scales of both shapes."""
+    print(f"[groups] {kind} kernel {kernel}: {M} {E} {N} {K}", flush=True)
+    assert w8.probe_grouped_kernel(kind, M, N, K, E) == kernel
+    offsets = _offsets(ref.uneven(M, E))
+    c = Case(kind, M, E, N, K, seed=kernel, whole=True)
+    c.check(w8, offsets, M, exact=True)
+    offsets[0], offsets[-1] = 1, M - 1
+    c.check(w8, offsets, M, rows=_rows(M, M, K), exact=True)
+    c = Case(kind, M // 2 + 1, E, N, K, seed=kernel + 1, channels=kind != "mx")
+    rows = _rows(M, c.X, K)
+    rows[M // 3], rows[M // 2] = -1, c.X
+    c.check(w8, offsets, M, rows=rows, bias=c.bias)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("E,M", [(64, 100), (65, 100), (130, 200), (1000, 700), (4096, 300)])
 def test_many_groups(w8, kind, E, M):

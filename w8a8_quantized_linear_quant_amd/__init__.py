@@ -28,6 +28,7 @@ the current stream.  The functions carry the C names:
   w8a8_linear_grouped_backward_dx / mxfp4_linear_grouped_backward_dx   their input gradients
   probe_mfma_i8                 diagnostic: sustained int8 MFMA loop (include/w8a8_probe.h)
   probe_cvt_e4m3                diagnostic: the hardware e4m3 conversion on consecutive f32 bit patterns
+  probe_grouped_kernel          diagnostic: the kernel that a product of groups takes
   probe_gemm_tile_n             diagnostic: the tile width along N w8a8_linear picks for an M x N output
 
 Codes are torch.int8 (int8) or torch.float8_e4m3fn (e4m3); bf16 tensors are
@@ -105,6 +106,7 @@ def _load_library():
         "w8a8_linear_grouped_backward_dx": (I, [I, P, P, P, P, P, I64, I64, I64, I64, P, P]),
         "mxfp4_linear_grouped": (I, [P, I64, P, P, P, P, P, I64, P, I64, I64, I64, P, P]),
         "mxfp4_linear_grouped_backward_dx": (I, [P, P, P, P, P, I64, I64, I64, I64, P, P]),
+        "w8a8_probe_grouped_kernel": (I, [I, I64, I64, I64, I64]),
         "w8a8_probe_sink_count": (I64, []),
         "w8a8_probe_mfma_i8": (I, [P, P, I64, P, P]),
         "w8a8_probe_cvt_e4m3": (I, [ctypes.c_uint32, I64, P, P]),
@@ -989,3 +991,9 @@ def probe_gemm_tile_n(M, N):
     """Tile width along N (256 or 192) that w8a8_linear and
     w8a8_linear_backward_dx take for an M x N output on the current device."""
     return int(_lib.w8a8_probe_gemm_tile_n(int(M), int(N)))
+
+
+def probe_grouped_kernel(kind, M, N, K, E=1):
+    """The kernel (0 .. 6, include/w8a8_experts.h) that w8a8_linear_grouped ("int8", "e4m3") or mxfp4_linear_grouped
+    ("mx") takes for M rows in E groups; mxfp4_linear: "mx" with E = 1."""
+    return int(_lib.w8a8_probe_grouped_kernel(("int8", "e4m3", "mx").index(kind), int(M), int(N), int(K), int(E)))

@@ -1,5 +1,7 @@
 // grouped.hip -- entry points of the products of groups of rows, and of the
 // 4-bit product (one group): argument checks and the choice of the kernel.
+#include <cmath>
+
 #include "grouped.hpp"
 
 namespace w8a8 {
@@ -23,15 +25,71 @@ w8a8_status check(const void *xq, int64_t X, const void *wq, const void *out, co
     return W8A8_OK;
 }
 
+// Which kernel: the one of least estimated time (us).  What each takes is
+// fitted to measurements over E 1 .. 64, N 768 .. 12288, K 1024 .. 4096 and 2 ..
+// 2048 rows a group; over the 132 grouped ones the choice is 3% slower than the
+// best, geometric mean.  Some of them (best; the others' next):
+//   one group, N = K 4096, 4-bit:  24 rows 16 x 32 5.9 (128 deep 12.3);  192 rows
+//     64 x 64 11.0 (12.5);  1024 rows 128 deep 15.4 (128 18.3);  2048 rows 128
+//     25.6 (256 32.4)
+//   8 experts, N = K 4096, e4m3:  8 rows each 16 x 32 24.5 (32 x 32 26.6);  64 each
+//     128 deep 33.8 (128 38.0);  400 each 256 62.0 (128 85.6)
+// An estimate has two parts, joined so that the greater one counts and a near
+// second adds to it: the weights' bytes at the rate the kernel reaches, and
+// rounds of its tiles over the chip, each with a start and a time for each 128
+// bytes of K (a partly filled round of the tile kernels is faster: fewer
+// workgroups share the memory and the power).
+template <int QT>
+GroupedKind choose(const GroupedArgs &a) {
+    constexpr bool kMx = QT == kTypeMx4;
+    const double cus = device_cu_count(), M = a.M, E = a.E, N = a.N;
+    const double steps = (a.kb + 127) / 128;
+    // groups with rows, if the rows fall at random; a group leaves half a tile empty on average
+    const double active = a.E == 1 ? 1.0 : E * (1.0 - std::exp(-M / E));
+    auto tiles = [&](double rows, double columns) {
+        const double tm = a.E == 1 ? std::ceil(M / rows) : std::fmax(active, M / rows + 0.5 * active);
+        return tm * std::ceil(N / columns);
+    };
+    const double bytes = active * N * a.kb * (kMx ? 1.0625 : 1.0);
+    auto joined = [](double work, double memory) { return std::cbrt(work * work * work + memory * memory * memory); };
+    // rows kernels: first round, later ones (workgroups start as others end: no whole rounds), workgroups a CU
+    auto rows = [&](double rows, double columns, double a_cu, double t0, double t1, double r0, double r1) {
+        if (M / rows + E > (1 << 20)) return 1e30;  // a launch of 2^23 workgroups holds 8 column tiles of so many row tiles
+        const double rounds = tiles(rows, columns) / (a_cu * cus);
+        return joined(t0 + t1 * steps + (rounds > 1.0 ? (rounds - 1.0) * (r0 + r1 * steps) : 0.0),
+                      bytes / (kMx ? 4.2e6 : 4.8e6));
+    };
+    // n workgroups at once, `full` a full round's time, `few` one's of up to `free` of them
+    auto persistent = [](double n, double slots, double free, double few, double full) {
+        const double whole = std::floor(n / slots), rest = n - whole * slots;
+        return whole * full + (rest < 1.0 ? 0.0 : rest <= free ? few : few + (full - few) * (rest - free) / (slots - free));
+    };
+    double t[kGroupedKinds];
+    t[kRows16x16] = rows(16, 16, 5, 4.2, 0.05, 4.0, 0.13);
+    t[kRows16x32] = rows(16, 32, 3, 4.5, 0.05, 3.7, 0.115);
+    t[kRows32x32] = rows(32, 32, 2, 4.6, 0.08, 3.6, 0.13);
+    t[kRows64x64] = rows(64, 64, 1, 6.5, 0.17, 6.0, 0.16);
+    t[kTile128Deep] = joined(std::fmax(1.0, std::ceil(tiles(128, 128) / cus - 0.05)) * (3.9 + (kMx ? 0.53 : 0.45) * steps),
+                             bytes / (kMx ? 5.2e6 : 4.2e6));
+    t[kTile128] = joined(persistent(tiles(128, 128), 2 * cus, cus, 3.9 + (kMx ? 0.7 : 0.6) * steps,
+                                    kMx ? 6.3 + 1.2 * steps : 6.7 + 0.92 * steps),
+                         bytes / (kMx ? 5.2e6 : 4.8e6));
+    t[kTile256] = joined(persistent(tiles(256, 256) * (a.E == 1 ? 1.0 : 0.97), cus, 0.0,
+                                    kMx ? 8.0 + 1.25 * steps : 8.5 + 1.07 * steps,
+                                    kMx ? 10.0 + 1.9 * steps : 12.0 + 1.45 * steps),
+                         bytes / 4.2e6);
+    int best = 0;
+    for (int k = 1; k < kGroupedKinds; ++k)
+        if (t[k] < t[best]) best = k;
+    return static_cast<GroupedKind>(best);
+}
+
 template <int QT>
 w8a8_status launch_grouped(const GroupedArgs &a, hipStream_t stream) {
     if (a.M == 0 || a.N == 0) return W8A8_OK;
-    if (a.M > 64 * (int64_t)a.E) {
-        const int64_t tiles = ((a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
-        launch_grouped_tiles<QT>(a, tiles >= device_cu_count() ? kTile256 : kTile128Deep, stream);
-    } else {
-        launch_grouped_rows<QT>(a, stream);
-    }
+    const GroupedKind kind = choose<QT>(a);
+    if (kind >= kTile128Deep) launch_grouped_tiles<QT>(a, kind, stream);
+    else launch_grouped_rows<QT>(a, kind, stream);
     return launch_status();
 }
 
@@ -129,4 +187,17 @@ extern "C" w8a8_status mxfp4_linear_backward_dx(const uint8_t *dyq, const uint8_
                                                 const uint8_t *ws_t, int64_t M, int64_t N, int64_t K, uint16_t *dx,
                                                 hipStream_t stream) {
     return w8a8::mx_product(dyq, M, dys, wq_t, ws_t, nullptr, nullptr, 1, nullptr, M, K, N, dx, stream);
+}
+
+extern "C" int w8a8_probe_grouped_kernel(int type, int64_t M, int64_t N, int64_t K, int64_t E) {
+    using namespace w8a8;
+    if (M < 1 || N < 1 || K < 1 || E < 1 || M > (1 << 30) || N > (1 << 30) || K > (1 << 22) || E > kMaxGroups) return -1;
+    GroupedArgs a = {};
+    a.M = (int)M;
+    a.N = (int)N;
+    a.E = (int)E;
+    a.kb = (int)(type == kTypeMx4 ? K / 2 : K);
+    if (type == kTypeInt8) return choose<kTypeInt8>(a);
+    if (type == kTypeE4m3) return choose<kTypeE4m3>(a);
+    return type == kTypeMx4 ? choose<kTypeMx4>(a) : -1;
 }

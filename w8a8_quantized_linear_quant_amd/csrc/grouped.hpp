@@ -105,16 +105,20 @@ __device__ __forceinline__ GroupTile find_tile(GroupWindow &w, int tile, const i
     return t;
 }
 
-// grouped_rows.hip: few rows a group.  Launches for every size; grouped.hip decides.
-template <int QT>
-void launch_grouped_rows(const GroupedArgs &a, hipStream_t stream);
-// grouped_tiles.hip: many rows a group.
-enum TileKind {
-    kTile256,      // 256 x 256, a ring of two stages, one workgroup a CU
+// Kernels and their tiles.  All take every size; grouped.hip chooses.
+enum GroupedKind {
+    kRows16x16,    // grouped_rows.hip: rows x columns
+    kRows16x32,
+    kRows32x32,
+    kRows64x64,
+    kTile128Deep,  // grouped_tiles.hip: 128 x 128, a ring of four stages, one workgroup a CU
     kTile128,      // 128 x 128, a ring of two, two workgroups a CU
-    kTile128Deep,  // 128 x 128, a ring of four, one workgroup a CU
+    kTile256,      // 256 x 256, a ring of two, one workgroup a CU
+    kGroupedKinds
 };
 template <int QT>
-void launch_grouped_tiles(const GroupedArgs &a, TileKind kind, hipStream_t stream);
+void launch_grouped_rows(const GroupedArgs &a, GroupedKind kind, hipStream_t stream);
+template <int QT>
+void launch_grouped_tiles(const GroupedArgs &a, GroupedKind kind, hipStream_t stream);
 
 }  // namespace w8a8

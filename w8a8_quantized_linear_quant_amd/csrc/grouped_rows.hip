@@ -304,14 +304,14 @@ void launch(const GroupedArgs &a, hipStream_t stream) {
 }  // namespace
 
 template <int QT>
-void launch_grouped_rows(const GroupedArgs &a, hipStream_t stream) {
-    const int64_t mean = (a.M + a.E - 1) / a.E;
-    if (mean <= 16) launch<QT, 1, 2>(a, stream);
-    else if (mean <= 32) launch<QT, 2, 2>(a, stream);
-    else launch<QT, 4, 2>(a, stream);
+void launch_grouped_rows(const GroupedArgs &a, GroupedKind kind, hipStream_t stream) {
+    if (kind == kRows16x16) launch<QT, 1, 1>(a, stream);
+    else if (kind == kRows16x32) launch<QT, 1, 2>(a, stream);
+    else if (kind == kRows32x32) launch<QT, 2, 2>(a, stream);
+    else launch<QT, 4, 4>(a, stream);
 }
-template void launch_grouped_rows<kTypeInt8>(const GroupedArgs &, hipStream_t);
-template void launch_grouped_rows<kTypeE4m3>(const GroupedArgs &, hipStream_t);
-template void launch_grouped_rows<kTypeMx4>(const GroupedArgs &, hipStream_t);
+template void launch_grouped_rows<kTypeInt8>(const GroupedArgs &, GroupedKind, hipStream_t);
+template void launch_grouped_rows<kTypeE4m3>(const GroupedArgs &, GroupedKind, hipStream_t);
+template void launch_grouped_rows<kTypeMx4>(const GroupedArgs &, GroupedKind, hipStream_t);
 
 }  // namespace w8a8

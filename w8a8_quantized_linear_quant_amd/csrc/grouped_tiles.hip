@@ -292,12 +292,12 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
             else wb[f - kNB] = *reinterpret_cast<const int *>(lp + (wm * WT + (f - kNB) * 32) * 16);
         }
     };
-    const int unit = 127;  // the scale 1
     auto product = [&](acc_t &c, const frag_t &a, const frag_t &b, int wa, int wb, auto step, auto first) __attribute__((always_inline)) {
         // (the host's pass knows no 32-byte register operands, and would drop the kernel's launch stub without a word)
 #ifdef __HIP_DEVICE_COMPILE__
         constexpr int s = decltype(step)::value;
         constexpr bool kFirst = decltype(first)::value;
+        const int unit = 127;  // the scale 1
         if constexpr (kInt8) {
             if constexpr (kFirst) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
             else asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
@@ -655,13 +655,13 @@ void launch(const GroupedArgs &a, hipStream_t stream) {
 }  // namespace
 
 template <int QT>
-void launch_grouped_tiles(const GroupedArgs &a, TileKind kind, hipStream_t stream) {
+void launch_grouped_tiles(const GroupedArgs &a, GroupedKind kind, hipStream_t stream) {
     if (kind == kTile256) launch<QT, 128, 2>(a, stream);
     else if (kind == kTile128) launch<QT, 64, 2>(a, stream);
     else launch<QT, 64, 4>(a, stream);
 }
-template void launch_grouped_tiles<kTypeInt8>(const GroupedArgs &, TileKind, hipStream_t);
-template void launch_grouped_tiles<kTypeE4m3>(const GroupedArgs &, TileKind, hipStream_t);
-template void launch_grouped_tiles<kTypeMx4>(const GroupedArgs &, TileKind, hipStream_t);
+template void launch_grouped_tiles<kTypeInt8>(const GroupedArgs &, GroupedKind, hipStream_t);
+template void launch_grouped_tiles<kTypeE4m3>(const GroupedArgs &, GroupedKind, hipStream_t);
+template void launch_grouped_tiles<kTypeMx4>(const GroupedArgs &, GroupedKind, hipStream_t);
 
 }  // namespace w8a8
