@@ -275,8 +275,11 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
             else y[e] = __builtin_fmaf((float)s[e], p.per_channel ? tm * p.sw[at] : tm, bias);
         }
         uint16_t *dst = p.out + (size_t)m * p.N + n;
-        if ((p.N & 3) == 0) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        if (n + 3 < p.N) {
+            // at the alignment of one value: rows of any N start anywhere
+            typedef uint32_t v2u_at2 __attribute__((ext_vector_type(2), aligned(2)));
+            typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+            *reinterpret_cast<v2u_at2 *>(dst) = v2u{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)

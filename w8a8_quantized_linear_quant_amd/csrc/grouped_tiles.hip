@@ -75,6 +75,16 @@ __device__ __forceinline__ float from_accumulator(int a) {
     asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
     return (float)v;
 }
+// 8 values to a row that has `left` columns from dst on, at the alignment of one (rows of any N start anywhere).
+__device__ __forceinline__ void store_row(uint16_t *dst, v4u d, int left) {
+    if (left >= 8) {
+        Bf16::store_chunk(dst, d);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) dst[i] = (uint16_t)(d[i >> 1] >> ((i & 1) * 16));
+    }
+}
 // A buffer of a few bytes: reads past them are 0.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t small_rsrc(const void *p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, bytes, kBufferRsrcWord3);
@@ -622,14 +632,11 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
                     const int m = mw + ps * 32 + row, n = nw + cp * kPassCols + ch * 8;
                     if (m >= c.end) continue;
                     uint16_t *dst = p.out + (size_t)m * N + n;
-                    if ((N & 7) == 0) {
-                        // whole 128-byte lines past the caches; parts of lines through them, to be merged there
-                        if (n < N && (N & 63) == 0) __builtin_nontemporal_store(d, reinterpret_cast<v4u *>(dst));
-                        else if (n < N) *reinterpret_cast<v4u *>(dst) = d;
+                    // whole 128-byte lines past the caches; parts of lines through them, to be merged there
+                    if ((N & 63) == 0) {
+                        if (n < N) __builtin_nontemporal_store(d, reinterpret_cast<v4u *>(dst));
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n + i < N) dst[i] = (uint16_t)(d[i >> 1] >> ((i & 1) * 16));
+                        store_row(dst, d, N - n);
                     }
                 }
                 __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
