@@ -141,8 +141,9 @@ w8a8_status mxfp4_linear_grouped_backward_dx(const uint8_t *dyq, const uint8_t *
  * device (type 0 int8, 1 e4m3, 2 the 4-bit format; E = 1 for mxfp4_linear), so
  * that a test can tell what a shape exercises: 0 .. 3 tiles of 16 x 16, 16 x
  * 32, 32 x 32, 64 x 64 with operands staged by each wave; 4 and 5 128 x 128
- * with a ring of four and of two stages; 6 256 x 256.  -1 for sizes below 1 or
- * another type.  Enqueues nothing.
+ * with a ring of four and of two stages; 6 256 x 256; 7 256 x 256 for whole
+ * rounds over the chip, and a rest of at most half a round in 128 x 128.  -1 for
+ * sizes below 1 or another type.  Enqueues nothing.
  */
 int w8a8_probe_grouped_kernel(int type, int64_t M, int64_t N, int64_t K, int64_t E);
 

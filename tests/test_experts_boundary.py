@@ -153,7 +153,7 @@ def test_binding_wants_gpu_tensors():
 def test_the_kernels_that_the_gpu_tests_name():
     for kind, kernel, M, E, N, K in ref.KERNELS:
         assert w8.probe_grouped_kernel(kind, M, N, K, E) == kernel, (kind, kernel, M, E, N, K)
-    assert {k[:2] for k in ref.KERNELS} == {(t, k) for t in ("int8", "e4m3", "mx") for k in range(7)}
+    assert {k[:2] for k in ref.KERNELS} == {(t, k) for t in ("int8", "e4m3", "mx") for k in range(8)}
 
 
 def test_probe_rejects():

@@ -994,6 +994,6 @@ def probe_gemm_tile_n(M, N):
 
 
 def probe_grouped_kernel(kind, M, N, K, E=1):
-    """The kernel (0 .. 6, include/w8a8_experts.h) that w8a8_linear_grouped ("int8", "e4m3") or mxfp4_linear_grouped
+    """The kernel (0 .. 7, include/w8a8_experts.h) that w8a8_linear_grouped ("int8", "e4m3") or mxfp4_linear_grouped
     ("mx") takes for M rows in E groups; mxfp4_linear: "mx" with E = 1."""
     return int(_lib.w8a8_probe_grouped_kernel(("int8", "e4m3", "mx").index(kind), int(M), int(N), int(K), int(E)))

@@ -27,13 +27,15 @@ w8a8_status check(const void *xq, int64_t X, const void *wq, const void *out, co
 
 // Which kernel: the one of least estimated time (us).  What each takes is
 // fitted to measurements over E 1 .. 64, N 768 .. 12288, K 1024 .. 4096 and 2 ..
-// 2048 rows a group; over the 132 grouped ones the choice is 3% slower than the
-// best, geometric mean.  Some of them (best; the others' next):
+// 2048 rows a group; on 70 other shapes (E 1 .. 64, N 192 .. 6144, K 256 .. 5120, 1
+// .. 16384 rows) the choice took 4% more than the best of all, geometric mean.
+// Some measurements (best; another):
 //   one group, N = K 4096, 4-bit:  24 rows 16 x 32 5.9 (128 deep 12.3);  192 rows
 //     64 x 64 11.0 (12.5);  1024 rows 128 deep 15.4 (128 18.3);  2048 rows 128
 //     25.6 (256 32.4)
 //   8 experts, N = K 4096, e4m3:  8 rows each 16 x 32 24.5 (32 x 32 26.6);  64 each
 //     128 deep 33.8 (128 38.0);  400 each 256 62.0 (128 85.6)
+//   8 experts of 2048 rows, N 1280, K 4096, int8:  256 with a rest 95.1 (256 106.2)
 // An estimate has two parts, joined so that the greater one counts and a near
 // second adds to it: the weights' bytes at the rate the kernel reaches, and
 // rounds of its tiles over the chip, each with a start and a time for each 128
@@ -69,15 +71,26 @@ GroupedKind choose(const GroupedArgs &a) {
     t[kRows16x32] = rows(16, 32, 3, 4.5, 0.05, 3.7, 0.115);
     t[kRows32x32] = rows(32, 32, 2, 4.6, 0.08, 3.6, 0.13);
     t[kRows64x64] = rows(64, 64, 1, 6.5, 0.17, 6.0, 0.16);
-    t[kTile128Deep] = joined(std::fmax(1.0, std::ceil(tiles(128, 128) / cus - 0.05)) * (3.9 + (kMx ? 0.53 : 0.45) * steps),
+    const double n128 = tiles(128, 128);
+    t[kTile128Deep] = joined(std::ceil(n128 / cus + (a.E == 1 ? 0.0 : 0.03)) * (kMx ? 6.0 + 0.4 * steps : 4.7 + 0.43 * steps),
                              bytes / (kMx ? 5.2e6 : 4.2e6));
-    t[kTile128] = joined(persistent(tiles(128, 128), 2 * cus, cus, 3.9 + (kMx ? 0.7 : 0.6) * steps,
-                                    kMx ? 6.3 + 1.2 * steps : 6.7 + 0.92 * steps),
-                         bytes / (kMx ? 5.2e6 : 4.8e6));
-    t[kTile256] = joined(persistent(tiles(256, 256) * (a.E == 1 ? 1.0 : 0.97), cus, 0.0,
-                                    kMx ? 8.0 + 1.25 * steps : 8.5 + 1.07 * steps,
-                                    kMx ? 10.0 + 1.9 * steps : 12.0 + 1.45 * steps),
-                         bytes / 4.2e6);
+    // tile kernels: a start, then rounds
+    const double few128 = kMx ? 0.9 + 0.65 * steps : 0.4 + 0.6 * steps, full128 = kMx ? 2.5 + 1.35 * steps : 2.0 + 1.1 * steps;
+    t[kTile128] = joined(4.0 + persistent(n128, 2 * cus, cus, few128, full128), bytes / (kMx ? 5.2e6 : 4.8e6));
+    const double n256 = tiles(256, 256) * (a.E == 1 ? 1.0 : 0.97);
+    const double few256 = kMx ? 2.0 + 1.25 * steps : 1.0 + 1.1 * steps, full256 = kMx ? 4.0 + 1.85 * steps : 4.0 + 1.5 * steps;
+    t[kTile256] = joined(7.0 + persistent(n256, cus, 0.0, few256, full256), bytes / 4.2e6);
+    // Whole rounds of 256, the rest in quarters: 3 us for the second launch, 5 where it may find nothing.  Groups of unknown lengths: the rest may
+    // be anything, so half the time it is what the first launch does by itself.
+    const double whole = std::floor(n256 / cus), rest = n256 - whole * cus;
+    const double quarters = persistent(4.0 * rest, 2 * cus, cus, few128, full128);
+    t[kTile256Split] = 1e30;
+    if (whole >= 1.0 && a.E == 1 && 2.0 * rest <= cus && rest > 0.0) {
+        t[kTile256Split] = joined(10.0 + whole * full256 + quarters, bytes / 4.2e6);
+    } else if (whole >= 1.0 && a.E > 1) {
+        const double plain = few256 + (full256 - few256) * 0.5, split = 5.0 + few128 + (full128 - few128) * 0.5;
+        t[kTile256Split] = t[kTile256] + 5.0 - (split < plain ? 0.5 * (plain - split) : 0.0);
+    }
     int best = 0;
     for (int k = 1; k < kGroupedKinds; ++k)
         if (t[k] < t[best]) best = k;

@@ -114,6 +114,7 @@ enum GroupedKind {
     kTile128Deep,  // grouped_tiles.hip: 128 x 128, a ring of four stages, one workgroup a CU
     kTile128,      // 128 x 128, a ring of two, two workgroups a CU
     kTile256,      // 256 x 256, a ring of two, one workgroup a CU
+    kTile256Split, // the same for whole rounds; a rest of at most half a round in a second launch, in 128 x 128
     kGroupedKinds
 };
 template <int QT>

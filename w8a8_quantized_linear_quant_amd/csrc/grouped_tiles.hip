@@ -95,10 +95,22 @@ __device__ __forceinline__ int load_i32(__amdgpu_buffer_rsrc_t r, int off) {
     return (int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
 
-template <int QT, int WT, int NST, bool TAIL>
-__global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void grouped_tiles_kernel(GroupedArgs p, int tiles_n) {
+// Of `all` tiles in rounds of `slots` workgroups, those of whole rounds if at
+// most half a round would be left, else all.
+__device__ __forceinline__ int kept_tiles(int all, int slots) {
+    const int whole = all / slots * slots, rest = all - whole;
+    return whole > 0 && 2 * rest <= slots ? whole : all;
+}
+
+// REST: the tiles of 256 that a launch of that size leaves, in quarters.
+// `split`: in that launch, whether it leaves them (kept_tiles).
+template <int QT, int WT, int NST, bool TAIL, bool REST>
+__global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void grouped_tiles_kernel(GroupedArgs p, int tiles_n,
+                                                                                             int split) {
+    static_assert(!REST || WT == 64, "quarters of 256 x 256 tiles");
     constexpr bool kInt8 = QT == kTypeInt8, kMx = QT == kTypeMx4;
     constexpr int BT = 2 * WT;                      // tile edge
+    constexpr int CT = REST ? 2 * BT : BT;          // edge of the tiles that are counted
     constexpr int kOpBytes = BT * kStageK;          // one operand's stage
     constexpr int kRowsWave = BT / 4;               // rows of each operand that a wave loads
     constexpr int kLoadsOp = kRowsWave / 8;         // 8 rows an instruction
@@ -127,14 +139,16 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
     const int stages = (kb + NST * kStageK - 1) / (NST * kStageK) * NST;
 
     GroupWindow win = {};
-    load_window<BT>(win, p.offsets, p.E, M, lane);
+    load_window<CT>(win, p.offsets, p.E, M, lane);
     int tiles_m;
     {
         GroupWindow w = win;
-        while (w.base + 64 < p.E) next_window<BT>(w, p.offsets, p.E, M, lane);
+        while (w.base + 64 < p.E) next_window<CT>(w, p.offsets, p.E, M, lane);
         tiles_m = __builtin_amdgcn_readlane(w.tiles, 63);
     }
-    const int total = tiles_m * tiles_n;
+    // this launch's tiles: numbers first .. first + total - 1 (REST: four quarters each)
+    const int all = tiles_m * tiles_n, kept = split ? kept_tiles(all, split) : all;
+    const int first = REST ? kept : 0, total = REST ? 4 * (all - kept) : kept;
     if ((int)blockIdx.x >= total) return;
 
     struct Tile {
@@ -144,16 +158,23 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
         Tile c = {0, 0, 0, 0};
         if (t >= total) return c;
         int tm, tn;
-        tile_at(t, tiles_m, tiles_n, tm, tn);
+        tile_at(REST ? first + t / 4 : t, tiles_m, tiles_n, tm, tn);
         if (tm < win.before) {
             win = GroupWindow{};
-            load_window<BT>(win, p.offsets, p.E, M, lane);
+            load_window<CT>(win, p.offsets, p.E, M, lane);
         }
-        const GroupTile g = find_tile<BT>(win, tm, p.offsets, p.E, M, lane);
+        const GroupTile g = find_tile<CT>(win, tm, p.offsets, p.E, M, lane);
         c.group = __builtin_amdgcn_readfirstlane(g.group);
         c.m0 = __builtin_amdgcn_readfirstlane(g.m0);
         c.end = __builtin_amdgcn_readfirstlane(g.end);
-        c.n0 = __builtin_amdgcn_readfirstlane(tn * BT);
+        c.n0 = __builtin_amdgcn_readfirstlane(tn * CT);
+        if constexpr (REST) {
+            // a quarter may lie past the group's rows or past N: nothing to do there
+            c.m0 += (t & 2) ? BT : 0;
+            c.n0 += (t & 1) ? BT : 0;
+            if (c.m0 >= c.end || c.n0 >= N) c.end = c.m0 = 0;
+            if (c.n0 >= N) c.n0 = 0;
+        }
         return c;
     };
 
@@ -647,25 +668,37 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
     __builtin_amdgcn_s_waitcnt(kWaitVm0);
 }
 
-template <int QT, int WT, int NST>
-void launch(const GroupedArgs &a, hipStream_t stream) {
-    constexpr int BT = 2 * WT;
-    const int tiles_n = (a.N + BT - 1) / BT;
+template <int QT, int WT, int NST, bool REST>
+void launch(const GroupedArgs &a, int split, hipStream_t stream) {
+    constexpr int BT = 2 * WT, CT = REST ? 2 * BT : BT;
+    const int tiles_n = (a.N + CT - 1) / CT;
     // every group may leave one tile partly filled
-    const int64_t most = (a.M / BT + (int64_t)(a.E < a.M ? a.E : a.M)) * tiles_n;
+    int64_t most = (a.M / CT + (int64_t)(a.E < a.M ? a.E : a.M)) * tiles_n;
+    if (REST && most > split / 2) most = split / 2;
+    if (REST) most *= 4;
     const int64_t slots = (int64_t)device_cu_count() * (WT == 64 && NST == 2 ? 2 : 1);
     const unsigned grid = (unsigned)(most < slots ? most : slots);
-    if (a.kb % (NST * kStageK) == 0) grouped_tiles_kernel<QT, WT, NST, false><<<grid, kThreads, 0, stream>>>(a, tiles_n);
-    else grouped_tiles_kernel<QT, WT, NST, true><<<grid, kThreads, 0, stream>>>(a, tiles_n);
+    if (a.kb % (NST * kStageK) == 0)
+        grouped_tiles_kernel<QT, WT, NST, false, REST><<<grid, kThreads, 0, stream>>>(a, tiles_n, split);
+    else
+        grouped_tiles_kernel<QT, WT, NST, true, REST><<<grid, kThreads, 0, stream>>>(a, tiles_n, split);
 }
 
 }  // namespace
 
 template <int QT>
 void launch_grouped_tiles(const GroupedArgs &a, GroupedKind kind, hipStream_t stream) {
-    if (kind == kTile256) launch<QT, 128, 2>(a, stream);
-    else if (kind == kTile128) launch<QT, 64, 2>(a, stream);
-    else launch<QT, 64, 4>(a, stream);
+    if (kind == kTile256Split) {
+        const int slots = device_cu_count();
+        launch<QT, 128, 2, false>(a, slots, stream);
+        launch<QT, 64, 2, true>(a, slots, stream);
+    } else if (kind == kTile256) {
+        launch<QT, 128, 2, false>(a, 0, stream);
+    } else if (kind == kTile128) {
+        launch<QT, 64, 2, false>(a, 0, stream);
+    } else {
+        launch<QT, 64, 4, false>(a, 0, stream);
+    }
 }
 template void launch_grouped_tiles<kTypeInt8>(const GroupedArgs &, GroupedKind, hipStream_t);
 template void launch_grouped_tiles<kTypeE4m3>(const GroupedArgs &, GroupedKind, hipStream_t);
