@@ -156,6 +156,22 @@ def test_many_groups(w8, kind, E, M):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("E,M,N,K", [(70, 3000, 1100, 160), (300, 20000, 260, 96), (200, 30000, 2100, 512)])
+def test_many_groups_with_many_rows(w8, kind, E, M, N, K):
+    """More groups than a wave's lanes, in the kernels whose workgroups walk
+    from tile to tile: the window of groups moves on, and back where tiles that
+    advance together lie on both sides of its edge."""
+    assert w8.probe_grouped_kernel(kind, M, N, K, E) >= 4
+    rng = random.Random(E)
+    lengths = [0] * E
+    for g in rng.choices(range(E), [rng.random() ** 3 for _ in range(E)], k=M):
+        lengths[g] += 1
+    c = Case(kind, M, E, N, K, seed=E, whole=True)
+    c.check(w8, _offsets(lengths), M, exact=True)
+    c.check(w8, _offsets(lengths), M, rows=_rows(M, M, E), exact=True)
+
+
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("M,N", [(60, 40), (700, 300)])
 def test_integers_that_make_no_sense(w8, kind, M, N):
     """Offsets that fall, lie outside [0, M] or overlap, and row indices outside
