@@ -767,8 +767,11 @@ def mxfp4_quantize(x, ldq=None, out=None, scale=None):
     M, K = x.shape
     px, ldx = _view(x, M, K, x.dtype, dev, "x", align=False)
     ldq = ldq if ldq is not None else K + (-K) % 32
-    out = _out(out, (*lead, ldq // 2), _U8, dev, "out")
-    scale = _out(scale, (*lead, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
+    if out is None and scale is None and len(lead) == 1:
+        out, scale = _new2(M, ldq // 2, _U8, dev), _new2(M, mxfp4_scale_stride(ldq), _U8, dev)
+    else:
+        out = _out(out, (*lead, ldq // 2), _U8, dev, "out")
+        scale = _out(scale, (*lead, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
     _check(_lib.mxfp4_quantize(xt, px, M, K, ldx, out.data_ptr(), ldq, scale.data_ptr(), _stream(dev)))
     return out, scale
 
@@ -802,13 +805,14 @@ def mxfp4_quantize_transposed(w, ldq=None, out=None, scale=None):
 def mxfp4_dequantize(codes, scale, K=None, dtype=torch.bfloat16, out=None):
     """The values of codes uint8 [..., ldq / 2] with their scales: dtype (bf16 or f32) [..., K], K = ldq by default.
     `out` (two dimensions) may have a row stride."""
-    dev, lead, ldq = _mx_operand(codes, scale, "codes", "scale")
+    dev, shape, ldq = _mx_operand(codes, scale, "codes", "scale")
     K = ldq if K is None else K
-    M = codes.numel() * 2 // ldq if ldq else 0
+    lead = shape[:-1]
+    M = shape[0] if len(shape) == 2 else lead.numel()
     if out is None:
-        out = torch.empty((*lead, K), dtype=dtype, device=dev)
+        out = _new2(M, K, dtype, dev) if len(shape) == 2 else torch.empty((*lead, K), dtype=dtype, device=dev)
     yt = _dtype_of(out, "out")
-    if len(lead) == 1:
+    if len(shape) == 2:
         py, ldy = _view(out, M, K, out.dtype, dev, "out", align=False)
     else:
         py, ldy = _out(out, (*lead, K), out.dtype, dev, "out").data_ptr(), K
@@ -816,37 +820,42 @@ def mxfp4_dequantize(codes, scale, K=None, dtype=torch.bfloat16, out=None):
     return out
 
 
+def _new2(rows, cols, dtype, device):
+    """An uninitialized matrix (0.3 us less than torch.empty of one shape)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _mx_operand(codes, scale, cname, sname, device=None):
-    """Checks a pair of codes [..., K / 2] and scales: (device, leading shape, K)."""
+    """Checks a pair of codes [..., K / 2] and scales: (device, shape of the codes, K)."""
     if not isinstance(codes, _Tensor) or not isinstance(scale, _Tensor):
         raise TypeError(f"{cname} and {sname} must be torch.Tensors")
     if codes.dtype is not _U8 or scale.dtype is not _U8:
         raise TypeError(f"{cname} and {sname} must be torch.uint8, got {codes.dtype} and {scale.dtype}")
-    dev = codes.device
     if not codes.is_cuda:
         raise ValueError(f"{cname} must be a GPU tensor")
+    dev = codes.device
     if scale.device != dev or (device is not None and dev != device):
         raise ValueError(f"{cname} is on {dev}, {sname} on {scale.device}" +
                          (f", the other operands on {device}" if device is not None else ""))
-    if codes.dim() < 2 or not codes.is_contiguous() or not scale.is_contiguous():
+    shape, have = codes.shape, scale.shape
+    if len(shape) < 2 or not codes.is_contiguous() or not scale.is_contiguous():
         raise ValueError(f"{cname} and {sname} must be contiguous, of two dimensions or more")
-    K = 2 * codes.shape[-1]
-    want = (*codes.shape[:-1], mxfp4_scale_stride(K))
-    if scale.shape != want:
-        raise ValueError(f"{sname} must have shape {tuple(want)} beside {cname} {tuple(codes.shape)}, "
-                         f"got {tuple(scale.shape)}")
-    return dev, codes.shape[:-1], K
+    K = 2 * shape[-1]
+    if have[-1:] != (mxfp4_scale_stride(K),) or have[:-1] != shape[:-1]:
+        raise ValueError(f"{sname} must have shape {(*shape[:-1], mxfp4_scale_stride(K))} beside {cname} "
+                         f"{tuple(shape)}, got {tuple(have)}")
+    return dev, shape, K
 
 
 def mxfp4_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
     """4-bit linear: xq [M, K / 2], wq [N, K / 2] with their scales (mxfp4_quantize) -> bf16 [M, N]."""
-    dev, lead, K = _mx_operand(xq, x_scale, "xq", "x_scale")
-    _, wlead, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
-    if len(lead) != 1 or len(wlead) != 1 or wk != K:
-        raise ValueError(f"xq must be [M, K / 2] and wq [N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
-    M, N = lead[0], wlead[0]
-    pb = _vec(bias, N, _BF16, dev, "bias")
-    y = _out(out, (M, N), _BF16, dev, "out")
+    dev, shape, K = _mx_operand(xq, x_scale, "xq", "x_scale")
+    _, wshape, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
+    if len(shape) != 2 or len(wshape) != 2 or wk != K:
+        raise ValueError(f"xq must be [M, K / 2] and wq [N, K / 2], got {tuple(shape)} and {tuple(wshape)}")
+    M, N = shape[0], wshape[0]
+    pb = None if bias is None else _vec(bias, N, _BF16, dev, "bias")
+    y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
     _check(_lib.mxfp4_linear(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, M, N, K,
                              y.data_ptr(), _stream(dev)))
     return y
@@ -883,15 +892,17 @@ def _groups(offsets, E, rows, bias, N, dev):
         raise TypeError("offsets must be a torch.int32 tensor")
     if offsets.device != dev or offsets.shape != (E + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets must be contiguous, on {dev}, of shape {(E + 1,)}, got {tuple(offsets.shape)}")
-    pr, M = None, None
+    pr = M = pb = None
     if rows is not None:
         pr = _vec(rows, 0, _I32, dev, "rows")
         if rows.dim() != 1:
             raise ValueError(f"rows must be 1-D, got {rows.dim()}-D")
         M = rows.shape[0]
-    if bias is not None and isinstance(bias, _Tensor) and bias.shape != (E, N):
-        raise ValueError(f"bias must have shape {(E, N)}, got {tuple(bias.shape)}")
-    return offsets.data_ptr(), pr, M, _vec(bias, E * N, _BF16, dev, "bias")
+    if bias is not None:
+        pb = _vec(bias, E * N, _BF16, dev, "bias")
+        if bias.shape != (E, N):
+            raise ValueError(f"bias must have shape {(E, N)}, got {tuple(bias.shape)}")
+    return offsets.data_ptr(), pr, M, pb
 
 
 def _codes8(t, dims, name, dtype=None, device=None):
@@ -927,7 +938,7 @@ def w8a8_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None,
     if isinstance(w_scale, _Tensor) and w_scale.shape != ((E, N) if per_channel else (E,)):
         raise ValueError(f"w_scale must have shape {(E,)} or {(E, N)}, got {tuple(w_scale.shape)}")
     pw = _vec(w_scale, E, _F32, dev, "w_scale")
-    y = _out(out, (M, N), _BF16, dev, "out")
+    y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
     _check(_lib.w8a8_linear_grouped(qt, xq.data_ptr(), X, ps, wq.data_ptr(), pw, per_channel, pb, po, E, pr, M, N, K,
                                     y.data_ptr(), _stream(dev)))
     return y
@@ -943,14 +954,14 @@ def w8a8_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale, offsets, out=N
 
 def mxfp4_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None, out=None):
     """w8a8_linear_grouped in the 4-bit format: xq [X, K / 2], wq [E, N, K / 2] with their scales (mxfp4_quantize)."""
-    dev, lead, K = _mx_operand(xq, x_scale, "xq", "x_scale")
-    _, wlead, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
-    if len(lead) != 1 or len(wlead) != 2 or wk != K:
-        raise ValueError(f"xq must be [X, K / 2] and wq [E, N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
-    X, (E, N) = lead[0], wlead
+    dev, shape, K = _mx_operand(xq, x_scale, "xq", "x_scale")
+    _, wshape, wk = _mx_operand(wq, w_scale, "wq", "w_scale", dev)
+    if len(shape) != 2 or len(wshape) != 3 or wk != K:
+        raise ValueError(f"xq must be [X, K / 2] and wq [E, N, K / 2], got {tuple(shape)} and {tuple(wshape)}")
+    X, E, N = shape[0], wshape[0], wshape[1]
     po, pr, M, pb = _groups(offsets, E, rows, bias, N, dev)
     M = X if M is None else M
-    y = _out(out, (M, N), _BF16, dev, "out")
+    y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
     _check(_lib.mxfp4_linear_grouped(xq.data_ptr(), X, x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, po, E,
                                      pr, M, N, K, y.data_ptr(), _stream(dev)))
     return y
