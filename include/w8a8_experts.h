@@ -102,7 +102,7 @@ w8a8_status mxfp4_linear_backward_dx(const uint8_t *dyq, const uint8_t *dys, con
  * zeros: nothing is read or written out of range, whatever they hold.
  *   xq codes [X, K], x_scale f32 [X]; wq codes [E, N, K], w_scale f32 [E], or
  *   [E, N] with per_channel; bias bf16 [E, N] or NULL; y bf16 [M, N].
- * Sums are int32 for int8 (exact while K <= 2^17), f32 for e4m3.
+ * Sums are int32 for int8 (exact while K < 2^17), f32 for e4m3.
  * Shape rules: 0 <= M, N, X <= 2^30 (X = M if rows is NULL); 16 <= K <= 2^22,
  * K % 16 == 0; 1 <= E <= 4096; with rows, X * K <= 2^31 (bytes of codes); at
  * most 2^31 - 1 tiles: (M / 16 + E) * ceil(N / 16).

@@ -323,22 +323,28 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
             else wb[f - kNB] = *reinterpret_cast<const int *>(lp + (wm * WT + (f - kNB) * 32) * 16);
         }
     };
+    if constexpr (!kMx) {
+        // e4m3: the scale 1.  Opaque: its register is written here and not again next to a product, which as assembly
+        // would not wait for that (nor does anything but the reads above write the other operands).
+        int unit = 127;
+        asm volatile("" : "+v"(unit));
+        sa[0][0] = sa[1][0] = unit;
+    }
     auto product = [&](acc_t &c, const frag_t &a, const frag_t &b, int wa, int wb, auto step, auto first) __attribute__((always_inline)) {
         // (the host's pass knows no 32-byte register operands, and would drop the kernel's launch stub without a word)
 #ifdef __HIP_DEVICE_COMPILE__
         constexpr int s = decltype(step)::value;
         constexpr bool kFirst = decltype(first)::value;
-        const int unit = 127;  // the scale 1
         if constexpr (kInt8) {
             if constexpr (kFirst) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
             else asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
         } else if constexpr (!kMx) {
             if constexpr (kFirst)
                 asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %3, %3 op_sel_hi:[0,0,0]"
-                             : "=a"(c) : "v"(a), "v"(b), "v"(unit));
+                             : "=a"(c) : "v"(a), "v"(b), "v"(wa));
             else
                 asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %3 op_sel_hi:[0,0,0]"
-                             : "+a"(c) : "v"(a), "v"(b), "v"(unit));
+                             : "+a"(c) : "v"(a), "v"(b), "v"(wa));
         } else if constexpr (kFirst) {
             static_assert(!kFirst || s == 0, "a tile starts with step 0");
             asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
