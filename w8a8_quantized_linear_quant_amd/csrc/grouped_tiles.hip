@@ -433,6 +433,8 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
                  }
                  constexpr int kPer = kInt8 ? 4 : 1;                // products of a group
                  constexpr int kGroups = kNB * kNB / kPer;
+                 // reads in the first three quarters of a step: the last ones are there when the next step wants them (1%)
+                 constexpr int kReadGroups = kGroups * 3 / 4;
                  constexpr int kL = NST == 4 ? kPart : kLast ? kLoads : 0, kL0 = NST == 4 ? kk * kPart : 0;
                  [&]<int... G>(std::integer_sequence<int, G...>) __attribute__((always_inline)) {
                      (([&]() __attribute__((always_inline)) {
@@ -446,11 +448,11 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
                           }(std::make_integer_sequence<int, kPer>{});
                           [&]<int... R>(std::integer_sequence<int, R...>) __attribute__((always_inline)) {
                               (([&]() __attribute__((always_inline)) {
-                                   constexpr int r = share_first(g, kReads, kGroups) + R;
+                                   constexpr int r = share_first(g, kReads, kReadGroups) + R;
                                    read_one(lp0, lp1, std::integral_constant<int, r>{}, fa[P ^ 1], fb[P ^ 1]);
                                }()),
                                ...);
-                          }(std::make_integer_sequence<int, share_count(g, kReads, kGroups)>{});
+                          }(std::make_integer_sequence<int, (g < kReadGroups ? share_count(g, kReads, kReadGroups) : 0)>{});
                           [&]<int... L>(std::integer_sequence<int, L...>) __attribute__((always_inline)) {
                               (load_one(refill, std::integral_constant<int, kL0 + share_first(g, kL, kGroups) + L>{}), ...);
                           }(std::make_integer_sequence<int, share_count(g, kL, kGroups)>{});
@@ -628,27 +630,32 @@ __global__ __launch_bounds__(kThreads, WT == 64 && NST == 2 ? 2 : 1) void groupe
 #pragma unroll
                     for (int cb = 0; cb < kCB; ++cb) {
                         const int mb = ps * kRB + rb, nb = cp * kCB + cb;
+                        float v[4 * kQuads];
+#pragma unroll
+                        for (int e = 0; e < 4 * kQuads; ++e) v[e] = from_accumulator(acc[nb][mb][e]);
+                        // (branches on the call's arguments spare an instruction a value each; int8 lost 2% with its own)
+                        if constexpr (kMx) {
+                            if (p.bias) {
+#pragma unroll
+                                for (int e = 0; e < 4 * kQuads; ++e) {
+                                    const uint32_t w = (e & 2) ? bias2[nb][e / 4].y : bias2[nb][e / 4].x;
+                                    v[e] += bf16_bits_to_f32((e & 1) ? w >> 16 : w & 0xFFFFu);
+                                }
+                            }
+                        } else if (kInt8 || p.per_channel) {
+#pragma unroll
+                            for (int e = 0; e < 4 * kQuads; ++e)
+                                v[e] = __builtin_fmaf(v[e], tm[mb] * channel[cb][e / 4][e % 4], bias[cb][e / 4][e % 4]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4 * kQuads; ++e) v[e] = __builtin_fmaf(v[e], tm[mb], bias[cb][e / 4][e % 4]);
+                        }
 #pragma unroll
                         for (int q = 0; q < kQuads; ++q) {
-                            v4f v;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = from_accumulator(acc[nb][mb][4 * q + i]);
-                            float y[4];
-                            if constexpr (kMx) {
-                                const uint2 b = bias2[nb][q];
-                                y[0] = v[0] + bf16_bits_to_f32(b.x & 0xFFFFu);
-                                y[1] = v[1] + bf16_bits_to_f32(b.x >> 16);
-                                y[2] = v[2] + bf16_bits_to_f32(b.y & 0xFFFFu);
-                                y[3] = v[3] + bf16_bits_to_f32(b.y >> 16);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    y[i] = __builtin_fmaf(v[i], tm[mb] * channel[cb][q][i], bias[cb][q][i]);
-                            }
                             const int row = rb * kBlk + brow, col = cb * kBlk + 8 * q + cq;
                             const int chunk = (col >> 3) ^ (row & (kOutChunks - 1));
                             *reinterpret_cast<uint2 *>(ob + row * kPassCols * 2 + chunk * 16 + (col & 7) * 2) =
-                                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                                make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
                         }
                     }
                 __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
