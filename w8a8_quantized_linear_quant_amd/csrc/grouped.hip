@@ -27,8 +27,9 @@ w8a8_status check(const void *xq, int64_t X, const void *wq, const void *out, co
 
 // Which kernel: the one of least estimated time (us).  What each takes is
 // fitted to measurements over E 1 .. 64, N 768 .. 12288, K 1024 .. 4096 and 2 ..
-// 2048 rows a group; on 70 other shapes (E 1 .. 64, N 192 .. 6144, K 256 .. 5120, 1
-// .. 16384 rows) the choice took 4% more than the best of all, geometric mean.
+// 2048 rows a group; on 180 shapes drawn from E 1 .. 61, N 137 .. 6144, K
+// 256 .. 4960 and 1 .. 15564 rows the choice took 3% more than the best of all,
+// geometric mean (1.24 times as much at worst).
 // Some measurements (best; another):
 //   one group, N = K 4096, 4-bit:  24 rows 16 x 32 5.9 (128 deep 12.3);  192 rows
 //     64 x 64 11.0 (12.5);  1024 rows 128 deep 15.4 (128 18.3);  2048 rows 128
@@ -53,13 +54,18 @@ GroupedKind choose(const GroupedArgs &a) {
         return tm * std::ceil(N / columns);
     };
     const double bytes = active * N * a.kb * (kMx ? 1.0625 : 1.0);
-    auto joined = [](double work, double memory) { return std::cbrt(work * work * work + memory * memory * memory); };
-    // rows kernels: first round, later ones (workgroups start as others end: no whole rounds), workgroups a CU
+    // (compared as cubes)
+    auto joined = [](double work, double memory) { return work * work * work + memory * memory * memory; };
+    // rows kernels: first round, later ones, workgroups a CU; a
+    // group's weights are read again for each of its row tiles, from closer memory
     auto rows = [&](double rows, double columns, double a_cu, double t0, double t1, double r0, double r1) {
-        if (M / rows + E > (1 << 20)) return 1e30;  // a launch of 2^23 workgroups holds 8 column tiles of so many row tiles
-        const double rounds = tiles(rows, columns) / (a_cu * cus);
+        if (M / rows + E > (1 << 20)) return 1e60;  // a launch of 2^23 workgroups holds 8 column tiles of so many row tiles
+        // (the busiest XCD's share: column tiles go to XCDs in turn)
+        const double share = tiles(rows, 8.0 * columns) * 8.0 / (a_cu * cus), again = tiles(rows, N) / active - 1.0;
+        // a round begun counts whole with one workgroup a CU, by half with more
+        const double rounds = a_cu > 1.0 ? 0.5 * (share + std::ceil(share)) : std::ceil(share);
         return joined(t0 + t1 * steps + (rounds > 1.0 ? (rounds - 1.0) * (r0 + r1 * steps) : 0.0),
-                      bytes / (kMx ? 4.2e6 : 4.8e6));
+                      bytes / (kMx ? 4.2e6 : 4.8e6) + again * bytes / (kMx ? 8.0e6 : 9.0e6));
     };
     // n workgroups at once, `full` a full round's time, `few` one's of up to `free` of them
     auto persistent = [](double n, double slots, double free, double few, double full) {
@@ -75,21 +81,22 @@ GroupedKind choose(const GroupedArgs &a) {
     t[kTile128Deep] = joined(std::ceil(n128 / cus + (a.E == 1 ? 0.0 : 0.03)) * (kMx ? 6.0 + 0.4 * steps : 4.7 + 0.43 * steps),
                              bytes / (kMx ? 5.2e6 : 4.2e6));
     // tile kernels: a start, then rounds
-    const double few128 = kMx ? 0.9 + 0.65 * steps : 0.4 + 0.6 * steps, full128 = kMx ? 2.5 + 1.35 * steps : 2.0 + 1.1 * steps;
+    const double few128 = kMx ? 0.9 + 0.65 * steps : 0.4 + 0.6 * steps, full128 = kMx ? 3.2 + 1.3 * steps : 2.0 + 1.1 * steps;
     t[kTile128] = joined(4.0 + persistent(n128, 2 * cus, cus, few128, full128), bytes / (kMx ? 5.2e6 : 4.8e6));
     const double n256 = tiles(256, 256) * (a.E == 1 ? 1.0 : 0.97);
-    const double few256 = kMx ? 2.0 + 1.25 * steps : 1.0 + 1.1 * steps, full256 = kMx ? 4.0 + 1.85 * steps : 4.0 + 1.5 * steps;
-    t[kTile256] = joined(7.0 + persistent(n256, cus, 0.0, few256, full256), bytes / 4.2e6);
-    // Whole rounds of 256, the rest in quarters: 3 us for the second launch, 5 where it may find nothing.  Groups of unknown lengths: the rest may
-    // be anything, so half the time it is what the first launch does by itself.
+    const double few256 = kMx ? 5.0 + 1.1 * steps : 4.0 + 1.02 * steps, full256 = kMx ? 8.5 + 1.55 * steps : 8.0 + 1.4 * steps;
+    const double work256 = 7.0 + persistent(n256, cus, 0.0, few256, full256);
+    t[kTile256] = joined(work256, bytes / 4.2e6);
+    // Whole rounds of 256, the rest in quarters: 3 us for the second launch, 5 where it may find nothing.  Groups of
+    // unknown lengths: the rest may be anything, so half the time it is what the first launch does by itself.
     const double whole = std::floor(n256 / cus), rest = n256 - whole * cus;
-    const double quarters = persistent(4.0 * rest, 2 * cus, cus, few128, full128);
-    t[kTile256Split] = 1e30;
+    t[kTile256Split] = 1e60;
     if (whole >= 1.0 && a.E == 1 && 2.0 * rest <= cus && rest > 0.0) {
+        const double quarters = persistent(4.0 * rest, 2 * cus, cus, few128, full128);
         t[kTile256Split] = joined(10.0 + whole * full256 + quarters, bytes / 4.2e6);
     } else if (whole >= 1.0 && a.E > 1) {
         const double plain = few256 + (full256 - few256) * 0.5, split = 5.0 + few128 + (full128 - few128) * 0.5;
-        t[kTile256Split] = t[kTile256] + 5.0 - (split < plain ? 0.5 * (plain - split) : 0.0);
+        t[kTile256Split] = joined(work256 + 5.0 - (split < plain ? 0.5 * (plain - split) : 0.0), bytes / 4.2e6);
     }
     int best = 0;
     for (int k = 1; k < kGroupedKinds; ++k)
