@@ -27,16 +27,17 @@ w8a8_status check(const void *xq, int64_t X, const void *wq, const void *out, co
 
 // Which kernel: the one of least estimated time (us).  What each takes is
 // fitted to measurements over E 1 .. 64, N 768 .. 12288, K 1024 .. 4096 and 2 ..
-// 2048 rows a group; on 180 shapes drawn from E 1 .. 61, N 137 .. 6144, K
-// 256 .. 4960 and 1 .. 15564 rows the choice took 3% more than the best of all,
-// geometric mean (1.24 times as much at worst).
+// 2048 rows a group; on 270 shapes drawn from E 1 .. 61, N 137 .. 6144, K
+// 256 .. 5056 and 1 .. 16384 rows the choice took 3% more than the best of all,
+// geometric mean (a quarter more at worst, among calls of 4 to 8 us).
 // Some measurements (best; another):
-//   one group, N = K 4096, 4-bit:  24 rows 16 x 32 5.9 (128 deep 12.3);  192 rows
-//     64 x 64 11.0 (12.5);  1024 rows 128 deep 15.4 (128 18.3);  2048 rows 128
-//     25.6 (256 32.4)
-//   8 experts, N = K 4096, e4m3:  8 rows each 16 x 32 24.5 (32 x 32 26.6);  64 each
-//     128 deep 33.8 (128 38.0);  400 each 256 62.0 (128 85.6)
-//   8 experts of 2048 rows, N 1280, K 4096, int8:  256 with a rest 95.1 (256 106.2)
+//   one group, 4-bit:  N = K 4096, 24 rows 16 x 32 5.8 (128 deep 11.8);  192 rows
+//     64 x 64 10.9 (128 deep 12.2);  1024 rows 128 deep 15.3 (128 17.9);  N 12288
+//     K 4096, 48 rows 64 x 64 11.6 (16 x 32 15.2)
+//   8 experts, N = K 4096, e4m3:  8 rows each 16 x 32 24.3 (32 x 32 27.1);  64 each
+//     128 deep 33.9 (128 38.1);  400 each 256 61.7 (128 85.9)
+//   32 experts of 25 rows, N 2048, K 4096, int8:  64 x 64 61.6 (128 75.7)
+//   8 experts of 2048 rows, N 1280, K 4096, int8:  256 with a rest 93.6 (256 101.0)
 // An estimate has two parts, joined so that the greater one counts and a near
 // second adds to it: the weights' bytes at the rate the kernel reaches, and
 // rounds of its tiles over the chip, each with a start and a time for each 128
@@ -78,11 +79,13 @@ GroupedKind choose(const GroupedArgs &a) {
     t[kRows32x32] = rows(32, 32, 2, 4.6, 0.08, 3.6, 0.13);
     t[kRows64x64] = rows(64, 64, 1, 6.5, 0.17, 6.0, 0.16);
     const double n128 = tiles(128, 128);
-    t[kTile128Deep] = joined(std::ceil(n128 / cus + (a.E == 1 ? 0.0 : 0.03)) * (kMx ? 6.0 + 0.4 * steps : 4.7 + 0.43 * steps),
-                             bytes / (kMx ? 5.2e6 : 4.2e6));
+    // (of groups of unknown lengths the tiles may be a few more or fewer)
+    const double deep = n128 / cus, rounds_deep =
+        a.E == 1 ? std::ceil(deep) : 0.5 * (std::ceil(0.93 * deep) + std::ceil(1.07 * deep));
+    t[kTile128Deep] = joined(rounds_deep * (kMx ? 6.0 + 0.4 * steps : 4.7 + 0.43 * steps), bytes / (kMx ? 5.2e6 : 4.2e6));
     // tile kernels: a start, then rounds
     const double few128 = kMx ? 0.9 + 0.65 * steps : 0.4 + 0.6 * steps, full128 = kMx ? 3.2 + 1.3 * steps : 2.0 + 1.1 * steps;
-    t[kTile128] = joined(4.0 + persistent(n128, 2 * cus, cus, few128, full128), bytes / (kMx ? 5.2e6 : 4.8e6));
+    t[kTile128] = joined(4.0 + persistent(n128, 2 * cus, cus, few128, full128), bytes / (kMx ? 5.2e6 : 3.9e6));
     const double n256 = tiles(256, 256) * (a.E == 1 ? 1.0 : 0.97);
     const double few256 = kMx ? 5.0 + 1.1 * steps : 4.0 + 1.02 * steps, full256 = kMx ? 8.5 + 1.55 * steps : 8.0 + 1.4 * steps;
     const double work256 = 7.0 + persistent(n256, cus, 0.0, few256, full256);
