@@ -79,9 +79,9 @@ GroupedKind choose(const GroupedArgs &a) {
     t[kRows32x32] = rows(32, 32, 2, 4.6, 0.08, 3.6, 0.13);
     t[kRows64x64] = rows(64, 64, 1, 6.5, 0.17, 6.0, 0.16);
     const double n128 = tiles(128, 128);
-    // (of groups of unknown lengths the tiles may be a few more or fewer)
-    const double deep = n128 / cus, rounds_deep =
-        a.E == 1 ? std::ceil(deep) : 0.5 * (std::ceil(0.93 * deep) + std::ceil(1.07 * deep));
+    // (of groups of unknown lengths, beyond half a tile on average, the tiles may be a few more or fewer)
+    const double deep = n128 / cus, around = a.E > 1 && M / 128.0 > 0.5 * active ? 0.07 : 0.0;
+    const double rounds_deep = 0.5 * (std::ceil((1.0 - around) * deep) + std::ceil((1.0 + around) * deep));
     t[kTile128Deep] = joined(rounds_deep * (kMx ? 6.0 + 0.4 * steps : 4.7 + 0.43 * steps), bytes / (kMx ? 5.2e6 : 4.2e6));
     // tile kernels: a start, then rounds
     const double few128 = kMx ? 0.9 + 0.65 * steps : 0.4 + 0.6 * steps, full128 = kMx ? 3.2 + 1.3 * steps : 2.0 + 1.1 * steps;
