@@ -1,5 +1,7 @@
 """The C ABI of include/w8a8_experts.h without a GPU: exports, sizes, and
 refusals before anything is launched."""
+import random
+
 import pytest
 import torch
 
@@ -160,3 +162,15 @@ def test_probe_rejects():
     for args in ((0, 0, 8, 64, 1), (0, 8, 0, 64, 1), (0, 8, 8, 0, 1), (0, 8, 8, 64, 0), (3, 8, 8, 64, 1), (-1, 8, 8, 64, 1),
                  (0, 8, 8, 64, 4097), (2, (1 << 30) + 1, 8, 64, 1)):
         assert lib.w8a8_probe_grouped_kernel(*args) == -1, args
+
+
+def test_few_rows_take_one_launch():
+    """Kernels 0 to 3 have a workgroup a tile, column tiles in eights: 2^23 at most (2^31 threads), whatever the sizes."""
+    rng, edge = random.Random(4), {0: (16, 16), 1: (16, 32), 2: (32, 32), 3: (64, 64)}
+    for _ in range(20000):
+        kind = rng.choice(("int8", "e4m3", "mx"))
+        E, M, N, K = (int(2 ** rng.uniform(lo, hi)) for lo, hi in ((0, 12), (0, 30), (4, 30), (0, 17)))
+        kernel = w8.probe_grouped_kernel(kind, M, N, 32 * K, E)
+        if kernel in edge:
+            rows, columns = edge[kernel]
+            assert (M // rows + min(E, M)) * (-(-N // (8 * columns)) * 8) <= 2 ** 23, (kind, M, N, K, E)

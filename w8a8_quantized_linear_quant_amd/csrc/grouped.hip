@@ -60,7 +60,7 @@ GroupedKind choose(const GroupedArgs &a) {
     // rows kernels: first round, later ones, workgroups a CU; a
     // group's weights are read again for each of its row tiles, from closer memory
     auto rows = [&](double rows, double columns, double a_cu, double t0, double t1, double r0, double r1) {
-        if (M / rows + E > (1 << 20)) return 1e60;  // a launch of 2^23 workgroups holds 8 column tiles of so many row tiles
+        if ((double)rows_tiles(a, (int)rows) * (N / columns + 8.0) > (1 << 23)) return 1e60;  // a launch's workgroups
         // (the busiest XCD's share: column tiles go to XCDs in turn)
         const double share = tiles(rows, 8.0 * columns) * 8.0 / (a_cu * cus), again = tiles(rows, N) / active - 1.0;
         // a round begun counts whole with one workgroup a CU, by half with more

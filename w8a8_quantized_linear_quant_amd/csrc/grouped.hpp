@@ -105,7 +105,11 @@ __device__ __forceinline__ GroupTile find_tile(GroupWindow &w, int tile, const i
     return t;
 }
 
-// Kernels and their tiles.  All take every size; grouped.hip chooses.
+// Tiles of `rows` rows that M rows in E groups can have: every group may leave one partly filled.
+inline int64_t rows_tiles(const GroupedArgs &a, int rows) { return a.M / rows + (int64_t)(a.E < a.M ? a.E : a.M); }
+
+// Kernels and their tiles; grouped.hip chooses.  Those of grouped_rows.hip take
+// what fits 2^23 workgroups (2^31 threads), the others every size.
 enum GroupedKind {
     kRows16x16,    // grouped_rows.hip: rows x columns
     kRows16x32,

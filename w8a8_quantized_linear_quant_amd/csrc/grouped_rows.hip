@@ -39,7 +39,7 @@ __device__ __forceinline__ v8i codes4(v4i d) {  // the operand of 4-bit codes: 1
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 template <int QT, int MB, int NB>
-__global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, int first_tile, int tiles_n, int columns) {
+__global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, int tiles_n, int columns) {
     constexpr bool kMx = QT == kTypeMx4;
     typedef typename std::conditional<QT == kTypeInt8, v4i, v4f>::type acc_t;
     constexpr int kRows = 16 * (MB + NB);             // x's, then the weight's
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // `columns` is tiles_n rounded up to a multiple of 8: the row tiles of one
     // column tile, which read the same weights, run on the same XCD
-    const int tm = blockIdx.x / columns, tn = first_tile + (int)(blockIdx.x - tm * columns);
+    const int tm = blockIdx.x / columns, tn = blockIdx.x - tm * columns;
     if (tn >= tiles_n) return;
     GroupWindow w = {};
     load_window<16 * MB>(w, p.offsets, p.E, p.M, lane);
@@ -292,18 +292,9 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
 
 template <int QT, int MB, int NB>
 void launch(const GroupedArgs &a, hipStream_t stream) {
-    const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
-    // every group may leave one tile partly filled
-    const int64_t tiles_m = a.M / (16 * MB) + (a.E < a.M ? a.E : a.M);
-    // 2^23 workgroups a launch at most: 2^31 threads
-    int64_t most = ((int64_t)1 << 23) / tiles_m / 8 * 8;
-    if (most < 8) most = 8;
-    for (int64_t first = 0; first < tiles_n; first += most) {
-        const int64_t here = tiles_n - first < most ? tiles_n - first : most;
-        const int columns = (int)((here + 7) / 8 * 8);
-        grouped_rows_kernel<QT, MB, NB><<<(unsigned)(tiles_m * columns), kThreads, 0, stream>>>(
-            a, (int)first, (int)(first + here), columns);
-    }
+    const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB), columns = (tiles_n + 7) / 8 * 8;
+    grouped_rows_kernel<QT, MB, NB>
+        <<<(unsigned)(rows_tiles(a, 16 * MB) * columns), kThreads, 0, stream>>>(a, tiles_n, columns);
 }
 
 }  // namespace

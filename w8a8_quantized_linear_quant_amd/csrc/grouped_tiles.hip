@@ -688,8 +688,7 @@ template <int QT, int WT, int NST, bool REST>
 void launch(const GroupedArgs &a, int split, hipStream_t stream) {
     constexpr int BT = 2 * WT, CT = REST ? 2 * BT : BT;
     const int tiles_n = (a.N + CT - 1) / CT;
-    // every group may leave one tile partly filled
-    int64_t most = (a.M / CT + (int64_t)(a.E < a.M ? a.E : a.M)) * tiles_n;
+    int64_t most = rows_tiles(a, CT) * tiles_n;
     if (REST && most > split / 2) most = split / 2;
     if (REST) most *= 4;
     const int64_t slots = (int64_t)device_cu_count() * (WT == 64 && NST == 2 ? 2 : 1);
