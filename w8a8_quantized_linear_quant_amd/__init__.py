@@ -837,13 +837,14 @@ def _mx_operand(codes, scale, cname, sname, device=None):
     if scale.device != dev or (device is not None and dev != device):
         raise ValueError(f"{cname} is on {dev}, {sname} on {scale.device}" +
                          (f", the other operands on {device}" if device is not None else ""))
-    shape, have = codes.shape, scale.shape
+    shape = codes.shape
     if len(shape) < 2 or not codes.is_contiguous() or not scale.is_contiguous():
         raise ValueError(f"{cname} and {sname} must be contiguous, of two dimensions or more")
     K = 2 * shape[-1]
-    if have[-1:] != (mxfp4_scale_stride(K),) or have[:-1] != shape[:-1]:
-        raise ValueError(f"{sname} must have shape {(*shape[:-1], mxfp4_scale_stride(K))} beside {cname} "
-                         f"{tuple(shape)}, got {tuple(have)}")
+    stride = -(-K // 512) * 16
+    want = (shape[0], stride) if len(shape) == 2 else (*shape[:-1], stride)
+    if scale.shape != want:
+        raise ValueError(f"{sname} must have shape {want} beside {cname} {tuple(shape)}, got {tuple(scale.shape)}")
     return dev, shape, K
 
 
