@@ -1,6 +1,9 @@
 // grouped_tiles.hip -- products of groups with many rows each: square output
-// tiles, both operands staged in LDS, bound by the matrix cores or, for the
-// smaller tile, by what a CU can load.
+// tiles, both operands staged in LDS, bound by the matrix cores and the power
+// they draw or, for the smaller tile, by the latency of loads that miss L2 (8192
+// x 12288 x 4096, 256 x 256: 4-bit 201 .. 220 us, 3.8 .. 4.1 PFLOP/s; int8 307 ..
+// 330, 2.5 .. 2.7 POPS; e4m3 295 .. 305.  2048 x 4096 x 4096 in 4 bits, 128 x 128:
+// 26 us, 2.6 PFLOP/s).
 //
 //  * Persistent: workgroups walk the tiles of all groups.  Which tiles there
 //    are lies on the device (offsets), so each workgroup counts them itself,
@@ -13,8 +16,9 @@
 //    instruction's first operand, so that a lane ends up with four consecutive
 //    columns of one row.
 //  * Codes go from memory to LDS without registers, 128 bytes of every row a
-//    stage, in a ring of two; 16-byte chunks are XOR-swizzled by row.  The ring
-//    runs ahead across tiles.  Gathered rows are a lane's own offset into x;
+//    stage, in a ring of two, or of four for 128 x 128 tiles where one a CU or
+//    fewer are left (512 rows, N = K 4096: int8 24.4 us with two, 19.9 with four);
+//    16-byte chunks are XOR-swizzled by row.  The ring runs ahead across tiles.  Gathered rows are a lane's own offset into x;
 //    their indices are loaded a tile ahead, one a lane.
 //  * 4-bit format: a stage is 256 values of K, 8 scales a row.  Lane half h of
 //    a 32 x 32 x 64 product takes block 4 h + s of them at step s -- which

@@ -8,7 +8,8 @@
 // a NaN (their bits are the largest as integers too).  x / 2^e is exact in f32
 // (v_ldexp_f32) and the hardware conversion rounds it to nearest even.
 //
-// All three are bound by memory (and below ~1 MB by the launch): one pass,
+// All three are bound by memory (and below ~1 MB by the launch; 5120 x 4096 bf16:
+// quantizer 11.3 us, 4.7 TB/s, transposed 13.4, dequantizer 11.0): one pass,
 // 16-byte loads, a unit of 512 columns a wave, so that a row's scales leave as
 // 16 bytes a unit.
 #include "../../include/w8a8_experts.h"
