@@ -295,6 +295,35 @@ def test_captured_with_new_routing(w8, kind, lengths):
         assert torch.equal(out, c.run(w8, off, rows, c.bias)), i
 
 
+def _uneven_offsets(M, E):
+    """What no estimate foresees: every row in the last group, in the first; a few rows; none; a range that runs
+    backwards; rows in the middle alone."""
+    return [[0] * E + [M], [0] + [M] * E, [0] + [37] * E, [5] * (E + 1), [0, M // 2, 3] + [M] * (E - 2),
+            [M // 3] * E + [M // 3 + 300]]
+
+
+@pytest.mark.parametrize("kernel", range(8))
+@pytest.mark.parametrize("kind", TYPES)
+def test_any_offsets_in_every_kernel(w8, kind, kernel):
+    """The kernel is chosen by the sizes alone, so each has to take whatever lies in `offsets`: eager, and captured
+    with other offsets."""
+    M, E, N, K = next(k[2:] for k in ref.KERNELS if k[:2] == (kind, kernel) and k[3] > 2)
+    c = Case(kind, M, E, N, K, seed=kernel, whole=True)
+    off = torch.tensor(_offsets(ref.uneven(M, E)), dtype=torch.int32, device="cuda")
+    out = torch.full((M, N), 7.25, dtype=torch.bfloat16, device="cuda")
+    c.run(w8, off, None, None, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(w8, off, None, None, out)
+    for offsets in _uneven_offsets(M, E):
+        y = c.check(w8, offsets, M, exact=True)
+        off.copy_(torch.tensor(offsets, dtype=torch.int32))
+        out.fill_(7.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y), offsets
+
+
 @pytest.mark.parametrize("kind", TYPES)
 def test_two_calls_at_once(w8, kind):
     a, b = Case(kind, 90, 3, 200, 256, seed=1), Case(kind, 400, 2, 264, 512, seed=2)

@@ -18,8 +18,9 @@
 //  * Codes go from memory to LDS without registers, 128 bytes of every row a
 //    stage, in a ring of two, or of four for 128 x 128 tiles where one a CU or
 //    fewer are left (512 rows, N = K 4096: int8 24.4 us with two, 19.9 with four);
-//    16-byte chunks are XOR-swizzled by row.  The ring runs ahead across tiles.  Gathered rows are a lane's own offset into x;
-//    their indices are loaded a tile ahead, one a lane.
+//    16-byte chunks are XOR-swizzled by row.  The ring runs ahead across tiles.
+//    Gathered rows are a lane's own offset into x; their indices are loaded a
+//    tile ahead, one a lane.
 //  * 4-bit format: a stage is 256 values of K, 8 scales a row.  Lane half h of
 //    a 32 x 32 x 64 product takes block 4 h + s of them at step s -- which
 //    block goes with which step is free as long as both operands agree -- so
