@@ -9,7 +9,7 @@
 // (v_ldexp_f32) and the hardware conversion rounds it to nearest even.
 //
 // All three are bound by memory (and below ~1 MB by the launch; 5120 x 4096 bf16:
-// quantizer 11.3 us, 4.7 TB/s, transposed 13.4, dequantizer 11.0): one pass,
+// quantizer 11.0 us, 4.8 TB/s, transposed 12.4, dequantizer 10.8): one pass,
 // 16-byte loads, a unit of 512 columns a wave, so that a row's scales leave as
 // 16 bytes a unit.
 #include "../../include/w8a8_experts.h"
@@ -123,10 +123,13 @@ __global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(const typ
                                                                        int64_t ldx, uint8_t *wq, int ldq, uint8_t *ws,
                                                                        int tiles_n, int tiles_k) {
     typedef typename X::type T;
-    // a row ends 4 bytes past a whole number of bank rounds: writes of 8 rows
-    // and reads of 64 columns both meet every bank
-    constexpr int kPitch = kTileK + 4 / sizeof(T);
-    __shared__ T tile[kTileN * kPitch];
+    // words XOR-swizzled by row, so that a write to several rows meets every bank, as a read of 64 columns of one row
+    // does by itself; no padding: bf16 takes 32 KB, five
+    // workgroups a CU (5120 x 4096: 11.8 us; three with padding and the results beside the tile, 12.8)
+    constexpr int kWord = 4 / sizeof(T);             // elements of a word
+    constexpr int kPitch = kTileK / kWord;           // words of a row
+    auto turn = [](int row) { return (row / kWord) & 3; };
+    __shared__ __attribute__((aligned(16))) uint32_t tile[kTileN * kPitch];
     const int64_t b = blockIdx.y;
     const int tk = blockIdx.x % tiles_k, tn = blockIdx.x / tiles_k;
     const int n0 = tn * kTileN, k0 = tk * kTileK;
@@ -143,15 +146,19 @@ __global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(const typ
     }
 #pragma unroll
     for (int i = 0; i < kTileN / kRows; ++i) {
-        T *dst = tile + (i * kRows + r0) * kPitch + c;
+        const int row = i * kRows + r0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(dst)[e] = d[i][e];
+        for (int e = 0; e < 4; ++e) tile[row * kPitch + c / kWord + (e ^ turn(row))] = d[i][e];
     }
     __syncthreads();
-    // one block of one result row a thread and step; its codes and scale back to LDS, so that they leave along rows
-    __shared__ v4u codes[kTileK * 8];  // [row][chunk, XOR-swizzled by row]
-    __shared__ __attribute__((aligned(8))) uint8_t scales[kTileK * 8];
+    // One block of one result row a thread and step; its codes and scale back to LDS, so that they leave along rows:
+    // in the tile's place.
+    v4u *codes = reinterpret_cast<v4u *>(tile);  // [row][chunk, XOR-swizzled by row]
+    uint8_t *scales = reinterpret_cast<uint8_t *>(codes + kTileK * 8);
+    static_assert(sizeof(tile) >= kTileK * 8 * 17, "results in the tile's place");
     const int k = threadIdx.x % kTileK;
+    v4u out[2];
+    int byte[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int nb = threadIdx.x / kTileK + 4 * i;  // block of the tile
@@ -159,15 +166,19 @@ __global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(const typ
         uint32_t amax = 0;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-            v[e] = X::load(tile + (nb * 32 + e) * kPitch + k);
+            v[e] = X::load(reinterpret_cast<const T *>(tile + (nb * 32 + e) * kPitch) + (k ^ (turn(e) * kWord)));
             amax = max(amax, abs_bits(v[e]));
         }
-        const int byte = scale_byte(amax);
-        v4u out;
+        byte[i] = scale_byte(amax);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = codes_of(v + 8 * e, byte);
-        codes[k * 8 + (nb ^ (k & 7))] = out;
-        scales[k * 8 + nb] = (uint8_t)(n0 + nb * 32 < ldq ? byte : kPadByte);
+        for (int e = 0; e < 4; ++e) out[i][e] = codes_of(v + 8 * e, byte[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int nb = threadIdx.x / kTileK + 4 * i;
+        codes[k * 8 + (nb ^ (k & 7))] = out[i];
+        scales[k * 8 + nb] = (uint8_t)(n0 + nb * 32 < ldq ? byte[i] : kPadByte);
     }
     __syncthreads();
     const int stride = (int)units_of(ldq) * 16;
