@@ -1,0 +1,154 @@
+"""Every kernel of the products of groups (named by probe_grouped_kernel) with
+what can go wrong in one and not in another: a bias and scales of every shape.
+
+Operands are whole numbers and powers of two, so that every result is known bit
+by bit: codes -8 .. 8 (4-bit format: every code, scales 2 and 4) have products
+that are whole multiples of 1 up to 64 (576), their sums over K <= 8224 stay
+below 2^24 in any order (8224 * 576 = 4.7e6), scales 2^-3 .. 2^3 of rows and
+weights only move the exponent, and one rounding to f32 (the multiply-add that
+takes the bias) and one to bf16 remain: those of `want`."""
+import pytest
+import torch
+
+import experts_helpers as ref
+
+pytestmark = pytest.mark.gpu
+KERNELS = ref.KERNELS
+
+
+@pytest.fixture(scope="module")
+def w8():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import w8a8_quantized_linear_quant_amd as w8
+    yield w8
+    torch.cuda.empty_cache()
+
+
+class Whole:
+    """Operands of one product, X rows of x."""
+
+    def __init__(self, kind, X, E, N, K, seed, channels=False):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.kind, self.X, self.E, self.N, self.K = kind, X, E, N, K
+
+        def integers(lo, hi, *shape):
+            return torch.randint(lo, hi, shape, generator=g, device="cuda")
+
+        if kind == "mx":
+            self.xq, self.wq = integers(0, 256, X, K // 2).to(torch.uint8), integers(0, 256, E, N, K // 2).to(torch.uint8)
+            self.xs = integers(128, 130, X, ref.stride_of(K)).to(torch.uint8)
+            self.ws = integers(128, 130, E, N, ref.stride_of(K)).to(torch.uint8)
+        else:
+            code = torch.int8 if kind == "int8" else torch.float8_e4m3fn
+            self.xq, self.wq = integers(-8, 9, X, K).to(torch.float32).to(code), integers(-8, 9, E, N, K).to(torch.float32).to(code)
+            self.xs = torch.pow(2.0, integers(-3, 4, X).float())
+            self.ws = torch.pow(2.0, integers(-3, 4, *((E, N) if channels else (E,))).float())
+        self.bias = integers(-100, 101, E, N).bfloat16()
+
+    def run(self, w8, offsets, rows=None, bias=None, out=None):
+        f = w8.mxfp4_linear_grouped if self.kind == "mx" else w8.w8a8_linear_grouped
+        return f(self.xq, self.xs, self.wq, self.ws, offsets, rows=rows, bias=bias, out=out)
+
+    def weight(self, g):
+        if self.kind == "mx":
+            return ref.values(self.wq[g], self.ws[g])
+        s = self.ws[g].double()
+        return self.wq[g].double() * (s[:, None] if s.dim() else s)
+
+    def want(self, offsets, M, rows=None, bias=None, rest=7.25):
+        """(the result, `rest` in rows of no group) in 64 bits."""
+        x = ref.values(self.xq, self.xs) if self.kind == "mx" else self.xq.double() * self.xs.double()[:, None]
+        if rows is not None:
+            r = rows.long()
+            inside = (r >= 0) & (r < self.X)
+            x = torch.where(inside[:, None], x[r.clamp(0, self.X - 1)], 0.0)
+        y = torch.full((M, self.N), rest, dtype=torch.float64, device="cuda")
+        for g, a, b in ref.groups_of(offsets, M):
+            if b > a:
+                y[a:b] = x[a:b] @ self.weight(g).T
+                if bias is not None:
+                    y[a:b] += bias[g].double()
+        return y
+
+    def check(self, w8, offsets, M, rows=None, bias=None):
+        out = torch.full((M, self.N), 7.25, dtype=torch.bfloat16, device="cuda")
+        y = self.run(w8, _device(offsets), rows, bias, out)
+        assert torch.equal(y, _rounded(self.want(offsets, M, rows, bias))), (self.kind, offsets)
+        return y
+
+
+def _rounded(want):
+    return want.float().bfloat16()
+
+
+def _device(offsets):
+    return torch.tensor(offsets, dtype=torch.int32, device="cuda")
+
+
+def _even(M, E):
+    out = [0]
+    for n in ref.uneven(M, E):
+        out.append(out[-1] + n)
+    return out
+
+
+def _rows(M, X, seed):
+    return torch.randint(0, X, (M,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32).cuda()
+
+
+def _named(w8, kind, kernel, M, E, N, K):
+    print(f"[kernels] {kind} {kernel}: {M} {E} {N} {K}", flush=True)
+    assert w8.probe_grouped_kernel(kind, M, N, K, E) == kernel
+
+
+@pytest.mark.parametrize("kind,kernel,M,E,N,K", KERNELS)
+def test_bias_and_scales_bit_by_bit(w8, kind, kernel, M, E, N, K):
+    """A bias alone, a bias beside scales of each output channel, in order and
+    gathered."""
+    _named(w8, kind, kernel, M, E, N, K)
+    offsets = _even(M, E)
+    c = Whole(kind, M, E, N, K, seed=kernel)
+    c.check(w8, offsets, M, bias=c.bias)
+    c = Whole(kind, M // 2 + 1, E, N, K, seed=kernel + 1, channels=kind != "mx")
+    offsets[0], offsets[-1] = 1, M - 1
+    c.check(w8, offsets, M, rows=_rows(M, c.X, K))
+    c.check(w8, offsets, M, rows=_rows(M, c.X, K), bias=c.bias)
+
+
+@pytest.mark.parametrize("kind,kernel,M,E,N,K", KERNELS)
+def test_random_products_near_the_definition(w8, kind, kernel, M, E, N, K):
+    """Relative Frobenius error 1e-3 against the definition rounded to bf16, this
+    library's measure of a product.  A result differs from the rounded
+    definition where a border between two bf16 values lies between the sums: by
+    a step s (2^-7 of the value at most) with the probability d / s of a
+    deviation d, so d may be 1e-6 of 2^-7, 1.3e-4 of the value.  f32 sums of 8224
+    terms stay far below it (2^-24 a term, at random: 6e-6); e4m3: products of 16
+    codes lose less than 2^-13 of the greatest of them each, evenly spread: 2^-13
+    / sqrt(3) = 7e-5 times the greatest of 16 products of normal values in units
+    of their root mean square, about 3, and of the products the half that lies
+    below 2^-5 of the greatest (those above lose nothing): 1.5e-4 of the sum's
+    own root mean square, an upper estimate."""
+    _named(w8, kind, kernel, M, E, N, K)
+    g = torch.Generator(device="cuda").manual_seed(kernel)
+    X = M // 2 + 1
+    x = torch.randn((X, K), generator=g, device="cuda")
+    w = torch.randn((E, N, K), generator=g, device="cuda") * 0.05
+    bias = torch.randn((E, N), generator=g, device="cuda").bfloat16()
+    c = Whole(kind, 1, 1, 1, 512, seed=0)
+    c.X, c.E, c.N, c.K = X, E, N, K
+    if kind == "mx":
+        c.xq, c.xs = w8.mxfp4_quantize(x)
+        c.wq, c.ws = w8.mxfp4_quantize(w)
+    else:
+        top, code = (127.0, torch.int8) if kind == "int8" else (448.0, torch.float8_e4m3fn)
+        c.xs, c.ws = x.abs().amax(1) / top, w.abs().amax(2) / top
+        c.xq, c.wq = x / c.xs[:, None], w / c.ws[..., None]
+        if kind == "int8":
+            c.xq, c.wq = c.xq.round(), c.wq.round()
+        c.xq, c.wq = c.xq.clamp(-top, top).to(code), c.wq.clamp(-top, top).to(code)
+    offsets, rows = _even(M, E), _rows(M, X, K)
+    y = c.run(w8, _device(offsets), rows, bias)
+    want = _rounded(c.want(offsets, M, rows, bias)).double()
+    off = float((y.double() - want).norm() / want.norm())
+    assert off <= 1e-3, off
