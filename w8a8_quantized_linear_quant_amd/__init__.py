@@ -2,7 +2,8 @@
 
 Argument marshalling only.  Every step of the path runs in the HIP kernels of
 the shared library (C ABI in include/w8a8.h); torch provides device memory and
-the current stream.  The functions carry the C names:
+the current stream of the operands' device, where every call runs.  The
+functions carry the C names:
 
   w8a8_quant_weight_tensorwise  tensor-wise int8 / e4m3 weight quantization
   w8a8_quant_act_rowwise        row-wise (token-wise) activation quantization
@@ -145,14 +146,24 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# the current stream's handle without building a torch.cuda.Stream (0.1 us against 2)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device and a device's current stream without building a torch.cuda.Stream (0.1 us against 2)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream(device):
-    if _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+def _launch(entry, device, *args):
+    """Calls a C entry point on the operands' device and that device's current stream, which is the entry point's last
+    argument.  The device has to be the current one meanwhile: the default stream's handle is the same for all, and
+    the library asks the current device for its size."""
+    index = device.index
+    if index == _raw_device():
+        status = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, _raw_stream(_raw_device() if index is None else index))
+    if status:
+        _check(status)
 
 
 def _qtype_of(codes):
@@ -242,8 +253,7 @@ def w8a8_quant_weight_tensorwise(w, qtype=INT8, transposed=False, out=None, out_
     wq_t = _out(out_t, (K, N), cd, dev, "out_t") if (transposed or out_t is not None) else None
     s = _buf(scale, 1, torch.float32, dev, "scale", alloc=4)
     ws = _buf(workspace, w8a8_weight_workspace_bytes(N, K), torch.uint8, dev, "workspace")
-    _check(_lib.w8a8_quant_weight_tensorwise(qtype, _ptr(w), N, K, _ptr(wq), _ptr(wq_t), _ptr(s), _ptr(ws),
-                                             _stream(dev)))
+    _launch(_lib.w8a8_quant_weight_tensorwise, dev, qtype, _ptr(w), N, K, _ptr(wq), _ptr(wq_t), _ptr(s), _ptr(ws))
     return wq, wq_t, s[:1]
 
 
@@ -266,7 +276,7 @@ def w8a8_quant_act_rowwise(x, qtype=INT8, ldq=None, out=None, scale=None):
     dev = x.device
     xq = _out(out, (M, ldq), cd, dev, "out")
     s = _buf(scale, M, torch.float32, dev, "scale")
-    _check(_lib.w8a8_quant_act_rowwise(qtype, _ptr(x), M, K, ldx, _ptr(xq), ldq, _ptr(s), _stream(dev)))
+    _launch(_lib.w8a8_quant_act_rowwise, dev, qtype, _ptr(x), M, K, ldx, _ptr(xq), ldq, _ptr(s))
     return xq, s[:M]
 
 
@@ -280,7 +290,7 @@ def w8a8_quant_act_rowwise_hadamard(x, qtype=INT8, ldq=None, out=None, scale=Non
     ldq = ldq if ldq is not None else K
     xq = _out(out, (M, ldq), cd, dev, "out")
     s = _buf(scale, M, torch.float32, dev, "scale")
-    _check(_lib.w8a8_quant_act_rowwise_hadamard(qtype, _ptr(x), M, K, K, _ptr(xq), ldq, _ptr(s), _stream(dev)))
+    _launch(_lib.w8a8_quant_act_rowwise_hadamard, dev, qtype, _ptr(x), M, K, K, _ptr(xq), ldq, _ptr(s))
     return xq, s[:M]
 
 
@@ -291,7 +301,7 @@ def w8a8_hadamard_rotate(x, out=None):
     x = _mat(_arg(x, torch.bfloat16, "x", dev), "x")
     M, K = x.shape
     y = _out(out, (M, K), torch.bfloat16, dev, "out")
-    _check(_lib.w8a8_hadamard_rotate(_ptr(x), M, K, K, _ptr(y), K, _stream(dev)))
+    _launch(_lib.w8a8_hadamard_rotate, dev, _ptr(x), M, K, K, _ptr(y), K)
     return y
 
 
@@ -319,8 +329,7 @@ def w8a8_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
     """Dequantized 8-bit linear.  xq [M, K], wq [N, K] codes (same dtype) -> bf16 [M, N]."""
     qt, dev, xq, x_scale, wq, w_scale, bias, M, N, K = _product_args(xq, x_scale, wq, w_scale, lambda n: 1, bias)
     y = _out(out, (M, N), torch.bfloat16, dev, "out")
-    _check(_lib.w8a8_linear(qt, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, _ptr(y),
-                            _stream(dev)))
+    _launch(_lib.w8a8_linear, dev, qt, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, _ptr(y))
     return y
 
 
@@ -340,8 +349,8 @@ def w8a8_linear_backward_dx(dyq, dy_scale, wq_t, w_scale, out=None):
     dy_scale = _arg(dy_scale, torch.float32, "dy_scale", dev, M)
     w_scale = _arg(w_scale, torch.float32, "w_scale", dev, 1)
     dx = _out(out, (M, K), torch.bfloat16, dev, "out")
-    _check(_lib.w8a8_linear_backward_dx(qt, _ptr(dyq), _ptr(dy_scale), _ptr(wq_t), _ptr(w_scale), M, N, K,
-                                        _ptr(dx), _stream(dev)))
+    _launch(_lib.w8a8_linear_backward_dx, dev, qt, _ptr(dyq), _ptr(dy_scale), _ptr(wq_t), _ptr(w_scale), M, N, K,
+            _ptr(dx))
     return dx
 
 
@@ -356,7 +365,7 @@ def w8a8_gemm_i32(xq, wq, out=None):
     if wq.shape[1] != K:
         raise ValueError("xq and wq must share K")
     acc = _out(out, (M, N), torch.int32, dev, "out")
-    _check(_lib.w8a8_gemm_i32(_ptr(xq), _ptr(wq), M, N, K, _ptr(acc), _stream(dev)))
+    _launch(_lib.w8a8_gemm_i32, dev, _ptr(xq), _ptr(wq), M, N, K, _ptr(acc))
     return acc
 
 
@@ -395,8 +404,8 @@ def svdq_linear(x, rq, r_scale, l1, l2, bias=None, out=None, xq_out=None, x_scal
     qt, dev, x, rq, r_scale, l1, l2, bias, M, N, K, r, y, xq, sx = _svdq_args(x, rq, r_scale, l1, l2, bias, out,
                                                                              xq_out, x_scale_out)
     ws = _buf(workspace, svdq_workspace_bytes(M, r), torch.uint8, dev, "workspace", alloc=16)
-    _check(_lib.svdq_linear(qt, _ptr(x), M, K, _ptr(rq), _ptr(r_scale), _ptr(l1), _ptr(l2), r, _ptr(bias), N,
-                            _ptr(y), _ptr(xq), _ptr(sx), _ptr(ws), _stream(dev)))
+    _launch(_lib.svdq_linear, dev, qt, _ptr(x), M, K, _ptr(rq), _ptr(r_scale), _ptr(l1), _ptr(l2), r, _ptr(bias), N,
+            _ptr(y), _ptr(xq), _ptr(sx), _ptr(ws))
     return y, xq, sx[:M]
 
 
@@ -406,8 +415,8 @@ def svdq_linear_noalloc(x, rq, r_scale, l1, l2, bias=None, out=None, xq_out=None
     `out`, `xq_out` and `x_scale_out` to allocate nothing here either."""
     qt, dev, x, rq, r_scale, l1, l2, bias, M, N, K, r, y, xq, sx = _svdq_args(x, rq, r_scale, l1, l2, bias, out,
                                                                              xq_out, x_scale_out)
-    _check(_lib.svdq_linear_noalloc(qt, _ptr(x), M, K, _ptr(rq), _ptr(r_scale), _ptr(l1), _ptr(l2), r, _ptr(bias),
-                                    N, _ptr(y), _ptr(xq), _ptr(sx), _stream(dev)))
+    _launch(_lib.svdq_linear_noalloc, dev, qt, _ptr(x), M, K, _ptr(rq), _ptr(r_scale), _ptr(l1), _ptr(l2), r,
+            _ptr(bias), N, _ptr(y), _ptr(xq), _ptr(sx))
     return y, xq, sx[:M]
 
 
@@ -437,8 +446,8 @@ def svdq_prepare(w, r, omega, iters=2, l1=None, l2=None, residual=None, sigma=No
     res = _out(residual, (N, K), torch.bfloat16, dev, "residual")
     sg = _buf(sigma, r, torch.float32, dev, "sigma", alloc=4)
     ws = _buf(workspace, svdq_prepare_workspace_bytes(N, K, r), torch.uint8, dev, "workspace", alloc=16)
-    _check(_lib.svdq_prepare(_ptr(w), N, K, r, _ptr(omega), iters, _ptr(l1), _ptr(l2), _ptr(res),
-                             _ptr(sg), _ptr(ws), _stream(dev)))
+    _launch(_lib.svdq_prepare, dev, _ptr(w), N, K, r, _ptr(omega), iters, _ptr(l1), _ptr(l2), _ptr(res), _ptr(sg),
+            _ptr(ws))
     return l1, l2, res, sg[:r]
 
 
@@ -454,7 +463,7 @@ def q8_0_quantize(x, out=None):
     x = _arg(x, torch.float32, "x", dev)
     n = x.numel()
     blocks = _buf(out, q8_0_nbytes(n), torch.uint8, dev, "out", alloc=16)
-    _check(_lib.q8_0_quantize(_ptr(x), n, _ptr(blocks), _stream(dev)))
+    _launch(_lib.q8_0_quantize, dev, _ptr(x), n, _ptr(blocks))
     return blocks[:q8_0_nbytes(n)]
 
 
@@ -464,7 +473,7 @@ def q8_0_dequantize(blocks, n, out=None):
     dev = blocks.device
     blocks = _arg(blocks, torch.uint8, "blocks", dev, q8_0_nbytes(n))
     y = _buf(out, n, torch.float32, dev, "out", alloc=4)
-    _check(_lib.q8_0_dequantize(_ptr(blocks), n, _ptr(y), _stream(dev)))
+    _launch(_lib.q8_0_dequantize, dev, _ptr(blocks), n, _ptr(y))
     return y[:n]
 
 
@@ -477,7 +486,7 @@ def gguf_a8_requant_q8_0(blocks, N, K, qtype=INT8, out=None, scale=None):
     blocks = _arg(blocks, torch.uint8, "blocks", dev, q8_0_nbytes(N * K) if K % 32 == 0 else 0)
     wq = _out(out, (N, K), cd, dev, "out")
     s = _buf(scale, N, torch.float32, dev, "scale", alloc=4)
-    _check(_lib.gguf_a8_requant_q8_0(qtype, _ptr(blocks), N, K, _ptr(wq), _ptr(s), _stream(dev)))
+    _launch(_lib.gguf_a8_requant_q8_0, dev, qtype, _ptr(blocks), N, K, _ptr(wq), _ptr(s))
     return wq, s[:N]
 
 
@@ -485,8 +494,8 @@ def gguf_a8_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
     """8-bit linear with per-output-channel weight scales w_scale f32 [N] -> bf16 [M, N]."""
     qt, dev, xq, x_scale, wq, w_scale, bias, M, N, K = _product_args(xq, x_scale, wq, w_scale, lambda n: n, bias)
     y = _out(out, (M, N), torch.bfloat16, dev, "out")
-    _check(_lib.gguf_a8_linear(qt, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, _ptr(y),
-                               _stream(dev)))
+    _launch(_lib.gguf_a8_linear, dev, qt, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K,
+            _ptr(y))
     return y
 
 
@@ -614,8 +623,8 @@ def lora_forward(x, a, b, plan, scale=None, ranks=None, base=None, out=None, u=N
     if u is None or workspace is not None:
         workspace = _buf(workspace, lora_forward_workspace_bytes(M, R), torch.uint8, dev, "workspace", alloc=16)
         pws = workspace.data_ptr()
-    _check(_lib.lora_forward(px, M, K, ldx, pa, pb, L, N, R, ps, pr, plan.data.data_ptr(), plan.tiles, pbase, ldbase,
-                             po, ldo, pu, pws, _stream(dev)))
+    _launch(_lib.lora_forward, dev, px, M, K, ldx, pa, pb, L, N, R, ps, pr, plan.data.data_ptr(), plan.tiles, pbase,
+            ldbase, po, ldo, pu, pws)
     return out, u
 
 
@@ -644,9 +653,9 @@ def lora_backward(dy, x, u, a, b, plan, scale=None, ranks=None, base=None, out=N
         da = db = None
     ws = _buf(workspace, lora_backward_workspace_bytes(M, plan.tiles, K, N, R, L), torch.uint8, dev,
               "workspace", alloc=16)
-    _check(_lib.lora_backward(pdy, M, N, lddy, px, K, ldx, pu, pa, pb, L, R, ps, pr, plan.data.data_ptr(), plan.tiles,
-                              pbase, ldbase, pdx, lddx, None if da is None else da.data_ptr(),
-                              None if db is None else db.data_ptr(), ws.data_ptr(), _stream(dev)))
+    _launch(_lib.lora_backward, dev, pdy, M, N, lddy, px, K, ldx, pu, pa, pb, L, R, ps, pr, plan.data.data_ptr(),
+            plan.tiles, pbase, ldbase, pdx, lddx, None if da is None else da.data_ptr(),
+            None if db is None else db.data_ptr(), ws.data_ptr())
     return dx, da, db
 
 
@@ -697,7 +706,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     if rstd is None:
         rstd = torch.empty_like(mean)
     pm, pr = _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd")
-    _check(_lib.layer_norm_forward(xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, pm, pr, _stream(dev)))
+    _launch(_lib.layer_norm_forward, dev, xt, px, M, K, ldx, wt, pw, pb, eps, py, ldy, pm, pr)
     return out, _first(mean, M), _first(rstd, M)
 
 
@@ -724,7 +733,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, dweight=None, 
     else:
         dweight = dbias = None
         args = None, None, None
-    _check(_lib.layer_norm_backward(xt, pdy, lddy, px, ldx, pm, pr, M, K, wt, pw, pdx, lddx, *args, _stream(dev)))
+    _launch(_lib.layer_norm_backward, dev, xt, pdy, lddy, px, ldx, pm, pr, M, K, wt, pw, pdx, lddx, *args)
     return dx, dweight, dbias
 
 
@@ -738,9 +747,8 @@ def w8a8_quant_act_rowwise_layer_norm(x, weight=None, bias=None, eps=1e-5, qtype
     xq = _out(out, (M, ldq), cd, dev, "out")
     if scale is None:
         scale = torch.empty(M, dtype=_F32, device=dev)
-    _check(_lib.w8a8_quant_act_rowwise_layer_norm(
-        qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq, _vec(scale, M, _F32, dev, "scale"),
-        _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd"), _stream(dev)))
+    _launch(_lib.w8a8_quant_act_rowwise_layer_norm, dev, qtype, xt, px, M, K, ldx, wt, pw, pb, eps, xq.data_ptr(), ldq,
+            _vec(scale, M, _F32, dev, "scale"), _vec(mean, M, _F32, dev, "mean"), _vec(rstd, M, _F32, dev, "rstd"))
     return xq, _first(scale, M)
 
 
@@ -772,7 +780,7 @@ def mxfp4_quantize(x, ldq=None, out=None, scale=None):
     else:
         out = _out(out, (*lead, ldq // 2), _U8, dev, "out")
         scale = _out(scale, (*lead, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
-    _check(_lib.mxfp4_quantize(xt, px, M, K, ldx, out.data_ptr(), ldq, scale.data_ptr(), _stream(dev)))
+    _launch(_lib.mxfp4_quantize, dev, xt, px, M, K, ldx, out.data_ptr(), ldq, scale.data_ptr())
     return out, scale
 
 
@@ -797,8 +805,8 @@ def mxfp4_quantize_transposed(w, ldq=None, out=None, scale=None):
     ldq = ldq if ldq is not None else N + (-N) % 32
     out = _out(out, (*lead, K, ldq // 2), _U8, dev, "out")
     scale = _out(scale, (*lead, K, mxfp4_scale_stride(ldq)), _U8, dev, "scale")
-    _check(_lib.mxfp4_quantize_transposed(wt, pw, lead[0] if lead else 1, N, K, ldx, out.data_ptr(), ldq,
-                                          scale.data_ptr(), _stream(dev)))
+    _launch(_lib.mxfp4_quantize_transposed, dev, wt, pw, lead[0] if lead else 1, N, K, ldx, out.data_ptr(), ldq,
+            scale.data_ptr())
     return out, scale
 
 
@@ -816,7 +824,7 @@ def mxfp4_dequantize(codes, scale, K=None, dtype=torch.bfloat16, out=None):
         py, ldy = _view(out, M, K, out.dtype, dev, "out", align=False)
     else:
         py, ldy = _out(out, (*lead, K), out.dtype, dev, "out").data_ptr(), K
-    _check(_lib.mxfp4_dequantize(codes.data_ptr(), scale.data_ptr(), M, K, ldq, yt, py, ldy, _stream(dev)))
+    _launch(_lib.mxfp4_dequantize, dev, codes.data_ptr(), scale.data_ptr(), M, K, ldq, yt, py, ldy)
     return out
 
 
@@ -857,8 +865,8 @@ def mxfp4_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
     M, N = shape[0], wshape[0]
     pb = None if bias is None else _vec(bias, N, _BF16, dev, "bias")
     y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
-    _check(_lib.mxfp4_linear(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, M, N, K,
-                             y.data_ptr(), _stream(dev)))
+    _launch(_lib.mxfp4_linear, dev, xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, M, N, K,
+            y.data_ptr())
     return y
 
 
@@ -940,8 +948,8 @@ def w8a8_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None,
         raise ValueError(f"w_scale must have shape {(E,)} or {(E, N)}, got {tuple(w_scale.shape)}")
     pw = _vec(w_scale, E, _F32, dev, "w_scale")
     y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
-    _check(_lib.w8a8_linear_grouped(qt, xq.data_ptr(), X, ps, wq.data_ptr(), pw, per_channel, pb, po, E, pr, M, N, K,
-                                    y.data_ptr(), _stream(dev)))
+    _launch(_lib.w8a8_linear_grouped, dev, qt, xq.data_ptr(), X, ps, wq.data_ptr(), pw, per_channel, pb, po, E, pr, M,
+            N, K, y.data_ptr())
     return y
 
 
@@ -963,8 +971,8 @@ def mxfp4_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None
     po, pr, M, pb = _groups(offsets, E, rows, bias, N, dev)
     M = X if M is None else M
     y = _new2(M, N, _BF16, dev) if out is None else _out(out, (M, N), _BF16, dev, "out")
-    _check(_lib.mxfp4_linear_grouped(xq.data_ptr(), X, x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb, po, E,
-                                     pr, M, N, K, y.data_ptr(), _stream(dev)))
+    _launch(_lib.mxfp4_linear_grouped, dev, xq.data_ptr(), X, x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), pb,
+            po, E, pr, M, N, K, y.data_ptr())
     return y
 
 
@@ -986,7 +994,7 @@ def probe_mfma_i8(a, b, pairs, sink=None):
             raise ValueError("probe operands: contiguous, at least 65536 bytes")
     n = _lib.w8a8_probe_sink_count()
     sink = _buf(sink, n, torch.int32, a.device, "sink")
-    _check(_lib.w8a8_probe_mfma_i8(_ptr(a), _ptr(b), int(pairs), _ptr(sink), _stream(a.device)))
+    _launch(_lib.w8a8_probe_mfma_i8, a.device, _ptr(a), _ptr(b), int(pairs), _ptr(sink))
     return sink
 
 
@@ -995,7 +1003,7 @@ def probe_cvt_e4m3(first_bits, n, out=None, device=None):
     first_bits, first_bits + 1, ..., by the quantizers' clamp and conversion."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     codes = _buf(out, n, torch.uint8, dev, "out", alloc=16)
-    _check(_lib.w8a8_probe_cvt_e4m3(ctypes.c_uint32(first_bits), n, _ptr(codes), _stream(dev)))
+    _launch(_lib.w8a8_probe_cvt_e4m3, dev, ctypes.c_uint32(first_bits), n, _ptr(codes))
     return codes[:n]
 
 
