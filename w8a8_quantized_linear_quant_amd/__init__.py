@@ -873,7 +873,15 @@ def mxfp4_linear(xq, x_scale, wq, w_scale, bias=None, out=None):
 def mxfp4_linear_backward_dx(dyq, dy_scale, wq_t, w_scale_t, out=None):
     """dX = dY . W: dyq [M, N / 2] (mxfp4_quantize of dY), wq_t [K, N / 2] (mxfp4_quantize_transposed of W) with their
     scales -> bf16 [M, K]."""
-    return mxfp4_linear(dyq, dy_scale, wq_t, w_scale_t, out=out)
+    dev, shape, N = _mx_operand(dyq, dy_scale, "dyq", "dy_scale")
+    _, wshape, wn = _mx_operand(wq_t, w_scale_t, "wq_t", "w_scale_t", dev)
+    if len(shape) != 2 or len(wshape) != 2 or wn != N:
+        raise ValueError(f"dyq must be [M, N / 2] and wq_t [K, N / 2], got {tuple(shape)} and {tuple(wshape)}")
+    M, K = shape[0], wshape[0]
+    dx = _new2(M, K, _BF16, dev) if out is None else _out(out, (M, K), _BF16, dev, "out")
+    _launch(_lib.mxfp4_linear_backward_dx, dev, dyq.data_ptr(), dy_scale.data_ptr(), wq_t.data_ptr(),
+            w_scale_t.data_ptr(), M, N, K, dx.data_ptr())
+    return dx
 
 
 # ------------------------------------------------------- products of groups
@@ -958,7 +966,22 @@ def w8a8_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale, offsets, out=N
     in the groups' order."""
     if isinstance(w_scale, _Tensor) and w_scale.dim() != 1:
         raise ValueError("w_scale must be [E]: a scale for each output channel does not leave the gradient's sum")
-    return w8a8_linear_grouped(dyq, dy_scale, wq_t, w_scale, offsets, out=out)
+    qt = _qtype_of(dyq) if isinstance(dyq, _Tensor) else None
+    dev = _codes8(dyq, 2, "dyq")
+    _codes8(wq_t, 3, "wq_t", dyq.dtype, dev)
+    M, N = dyq.shape
+    E, K = wq_t.shape[:2]
+    if wq_t.shape[2] != N:
+        raise ValueError(f"dyq and wq_t must share N, got {N} and {wq_t.shape[2]}")
+    po = _groups(offsets, E, None, None, K, dev)[0]
+    ps = _vec(dy_scale, M, _F32, dev, "dy_scale")
+    if isinstance(w_scale, _Tensor) and w_scale.shape != (E,):
+        raise ValueError(f"w_scale must have shape {(E,)}, got {tuple(w_scale.shape)}")
+    pw = _vec(w_scale, E, _F32, dev, "w_scale")
+    dx = _new2(M, K, _BF16, dev) if out is None else _out(out, (M, K), _BF16, dev, "out")
+    _launch(_lib.w8a8_linear_grouped_backward_dx, dev, qt, dyq.data_ptr(), ps, wq_t.data_ptr(), pw, po, E, M, N, K,
+            dx.data_ptr())
+    return dx
 
 
 def mxfp4_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None, out=None):
@@ -979,7 +1002,16 @@ def mxfp4_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None
 def mxfp4_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale_t, offsets, out=None):
     """dX[p] = dY[p] . W[g]: dyq [M, N / 2], wq_t [E, K, N / 2] (mxfp4_quantize_transposed) with their scales ->
     bf16 [M, K] in the groups' order."""
-    return mxfp4_linear_grouped(dyq, dy_scale, wq_t, w_scale_t, offsets, out=out)
+    dev, shape, N = _mx_operand(dyq, dy_scale, "dyq", "dy_scale")
+    _, wshape, wn = _mx_operand(wq_t, w_scale_t, "wq_t", "w_scale_t", dev)
+    if len(shape) != 2 or len(wshape) != 3 or wn != N:
+        raise ValueError(f"dyq must be [M, N / 2] and wq_t [E, K, N / 2], got {tuple(shape)} and {tuple(wshape)}")
+    M, E, K = shape[0], wshape[0], wshape[1]
+    po = _groups(offsets, E, None, None, K, dev)[0]
+    dx = _new2(M, K, _BF16, dev) if out is None else _out(out, (M, K), _BF16, dev, "out")
+    _launch(_lib.mxfp4_linear_grouped_backward_dx, dev, dyq.data_ptr(), dy_scale.data_ptr(), wq_t.data_ptr(),
+            w_scale_t.data_ptr(), po, E, M, N, K, dx.data_ptr())
+    return dx
 
 
 # ---------------------------------------------------------------- diagnostics
