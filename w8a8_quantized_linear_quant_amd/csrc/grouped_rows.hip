@@ -51,9 +51,7 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
     // two units a wave; one array each, so that the compiler can tell the loads into one from the reads of the other
     __shared__ __attribute__((aligned(1024))) uint8_t slot0[kWaves * kSlotBytes];
     __shared__ __attribute__((aligned(1024))) uint8_t slot1[kWaves * kSlotBytes];
-    static_assert(kPartBytes <= (int)sizeof(slot0) + (int)sizeof(slot1), "the sums take the units' place");
-    constexpr bool kPartFits = kPartBytes <= (int)sizeof(slot0);
-    __shared__ __attribute__((aligned(16))) uint8_t part_own[kPartFits ? 16 : kPartBytes];
+    static_assert(kPartBytes <= (int)sizeof(slot0), "the sums take the first units' place");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -238,10 +236,10 @@ __global__ __launch_bounds__(kThreads) void grouped_rows_kernel(GroupedArgs p, i
         step(s1, i + kWaves, std::integral_constant<int, kLoads>{});
     }
 
-    // The waves' sums, in the units' place once no load is on its way there.
+    // The waves' sums, in the first units' place once no load is on its way there.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    acc_t *part = reinterpret_cast<acc_t *>(kPartFits ? slot0 : part_own);
+    acc_t *part = reinterpret_cast<acc_t *>(slot0);
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
