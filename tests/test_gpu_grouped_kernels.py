@@ -131,10 +131,10 @@ def test_random_products_near_the_definition(w8, kind, kernel, M, E, N, K):
     definition where a border between two bf16 values lies between the sums: by
     a step s (2^-7 of the value at most) with the probability d / s of a
     deviation d, so d may be 1e-6 of 2^-7, 1.3e-4 of the value.  f32 sums of 8224
-    terms stay far below it (2^-24 a term, at random: 6e-6); e4m3: products of 16
+    terms stay far below it (2^-24 a term, at random: 6e-6); e4m3: products of 8
     codes lose less than 2^-13 of the greatest of them each, evenly spread: 2^-13
-    / sqrt(3) = 7e-5 times the greatest of 16 products of normal values in units
-    of their root mean square, about 3, and of the products the half that lies
+    / sqrt(3) = 7e-5 times the greatest of 8 products of normal values in units
+    of their root mean square, below 3, and of the products the half that lies
     below 2^-5 of the greatest (those above lose nothing): 1.5e-4 of the sum's
     own root mean square, an upper estimate."""
     _named(w8, kind, kernel, M, E, N, K)
