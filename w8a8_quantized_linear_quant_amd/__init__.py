@@ -886,13 +886,15 @@ def mxfp4_linear_backward_dx(dyq, dy_scale, wq_t, w_scale_t, out=None):
 
 # ------------------------------------------------------- products of groups
 def w8a8_quant_weight_grouped(w, qtype=INT8, transposed=False):
-    """w8a8_quant_weight_tensorwise of each of w bf16 [E, N, K].  Returns (codes [E, N, K], codes^T [E, K, N] or None,
-    scales f32 [E])."""
+    """w8a8_quant_weight_tensorwise of each of w bf16 [E, N, K], N * K % 16 == 0.  Returns (codes [E, N, K], codes^T
+    [E, K, N] or None, scales f32 [E])."""
     cd = _code_dtype(qtype)
     _need(w, _BF16, "w")
     if w.dim() != 3:
         raise ValueError(f"w must be 3-D, got {w.dim()}-D")
     E, N, K = w.shape
+    if E > 1 and N * K % 16 != 0:
+        raise ValueError(f"N * K must be a multiple of 16 (each weight and its codes start on a 16-byte boundary), got {N} x {K}")
     wq = torch.empty((E, N, K), dtype=cd, device=w.device)
     wq_t = torch.empty((E, K, N), dtype=cd, device=w.device) if transposed else None
     scale = torch.empty((E, 4), dtype=_F32, device=w.device)       # each starts on a 16-byte boundary
