@@ -123,6 +123,8 @@ w8a8_status w8a8_linear_grouped(w8a8_qtype qtype, const void *xq, int64_t X, con
  * dX[p, :] = dY[p, :] . W[g] from dyq codes [M, N], dy_scale f32 [M] and the
  * transposed codes wq_t [E, K, N] with w_scale f32 [E]; dx bf16 [M, K], in the
  * groups' order (the rows of one token are the caller's to add up).
+ * A forward call's scale for each channel does not leave this sum: multiply
+ * dY[p, n] by w_scale[g, n] before it is quantized, and pass scales of 1.
  * Shape rules as the forward call's with N and K exchanged.
  */
 w8a8_status w8a8_linear_grouped_backward_dx(w8a8_qtype qtype, const void *dyq, const float *dy_scale,

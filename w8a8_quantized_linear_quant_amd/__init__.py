@@ -965,9 +965,11 @@ def w8a8_linear_grouped(xq, x_scale, wq, w_scale, offsets, rows=None, bias=None,
 
 def w8a8_linear_grouped_backward_dx(dyq, dy_scale, wq_t, w_scale, offsets, out=None):
     """dX[p] = dY[p] . W[g]: dyq [M, N] codes, wq_t [E, K, N] transposed weight codes, w_scale f32 [E] -> bf16 [M, K]
-    in the groups' order."""
+    in the groups' order.  Beside a forward call with w_scale [E, N]: dY times the scales of its rows' groups is what is
+    quantized to dyq, and w_scale is 1."""
     if isinstance(w_scale, _Tensor) and w_scale.dim() != 1:
-        raise ValueError("w_scale must be [E]: a scale for each output channel does not leave the gradient's sum")
+        raise ValueError("w_scale must be [E]: a scale for each output channel does not leave the gradient's sum; "
+                         "multiply dY by it before dY is quantized and pass scales of 1")
     qt = _qtype_of(dyq) if isinstance(dyq, _Tensor) else None
     dev = _codes8(dyq, 2, "dyq")
     _codes8(wq_t, 3, "wq_t", dyq.dtype, dev)
