@@ -32,7 +32,7 @@ class Routing:
 
     def to_tokens(self, rows):
         """[T, top, width] of the rows [T * top, width]."""
-        return rows[self.slot_row].view(*self.shape, -1)
+        return rows[self.slot_row].view(*self.shape, rows.shape[1])
 
 
 class Experts:

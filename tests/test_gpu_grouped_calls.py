@@ -1,11 +1,15 @@
 """Calls of the products of groups that the documentation allows or refuses and
 that no product's own test makes."""
+import os
+import sys
+
 import pytest
 import torch
 
 import experts_helpers as ref
 
 pytestmark = pytest.mark.gpu
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 @pytest.fixture(scope="module")
@@ -71,3 +75,13 @@ def test_the_gradient_beside_scales_of_channels(w8, kind):
     assert bool(((dx.double() - want).abs() <= room + ref.BF16_HALF_STEP * (want.abs() + room)).all())
     with pytest.raises(ValueError, match="multiply dY"):
         w8.w8a8_linear_grouped_backward_dx(dq, ds, wt, s, off)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3", "mx"])
+def test_the_example_without_tokens(w8, kind):
+    import experts_block
+    b = experts_block.Experts(kind, 3, 64, 96)
+    x, choice, weight = experts_block.inputs(0, 64, 3, 2)
+    y, saved = b.forward(x, choice, weight)
+    dx, dweight = b.backward(torch.zeros_like(y), saved)
+    assert y.shape == (0, 64) and dx.shape == (0, 64) and dweight.shape == (0, 2)
