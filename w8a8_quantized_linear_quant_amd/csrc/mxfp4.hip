@@ -8,10 +8,12 @@
 // a NaN (their bits are the largest as integers too).  x / 2^e is exact in f32
 // (v_ldexp_f32) and the hardware conversion rounds it to nearest even.
 //
-// All three are bound by memory (and below ~1 MB by the launch; 5120 x 4096 bf16:
-// quantizer 11.0 us, 4.8 TB/s, transposed 12.4, dequantizer 10.8): one pass,
-// 16-byte loads, a unit of 512 columns a wave, so that a row's scales leave as
-// 16 bytes a unit.
+// All three are bound by memory (and below ~1 MB by the launch).  5120 x 4096 in
+// bf16 and f32, twelve sets of operands in turn, that is from HBM: quantizer
+// 12.1 and 19.9 us (4.4 and 4.8 TB/s), transposed 14.2 and 22.3, dequantizer
+// 11.8 and 22.8; three sets, partly from the Infinity Cache: 10.4 and 16.7,
+// 11.5 and 19.2, 10.3 and 21.8.  One pass, 16-byte loads, a unit of 512 columns
+// a wave, so that a row's scales leave as 16 bytes a unit.
 #include "../../include/w8a8_experts.h"
 #include "block.hpp"
 #include "internal.hpp"
@@ -21,7 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 512;      // columns of a row that a wave takes at a time: 16 scale bytes
-// units in flight a wave (5120 x 4096 bf16: quantizer 12.9 us with 1, 12.1 with 4, 13.7 with 8; dequantizer 14.0, 13.1, 11.7)
+// units in flight a wave (5120 x 4096 from HBM, bf16: quantizer 12.7 us with 1, 12.3 with 2, 12.1 with 4, 13.8 with 8;
+// dequantizer 14.0, 13.3, 13.1, 11.8; f32: 18.2, 18.5, 19.9, 21.3; 23.9, 26.0, 25.5, 22.8)
 constexpr int kQuantizeUnits = 4, kDequantizeUnits = 8;
 constexpr int kPadByte = 127;   // padding of a row's scales: the scale 1
 
@@ -125,7 +128,8 @@ __global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(const typ
     typedef typename X::type T;
     // words XOR-swizzled by row, so that a write to several rows meets every bank, as a read of 64 columns of one row
     // does by itself; no padding: bf16 takes 32 KB, five
-    // workgroups a CU (5120 x 4096: 11.8 us; three with padding and the results beside the tile, 12.8)
+    // workgroups a CU (5120 x 4096, three sets of operands: 11.5 us; three with padding and the results beside the tile,
+    // 12.4)
     constexpr int kWord = 4 / sizeof(T);             // elements of a word
     constexpr int kPitch = kTileK / kWord;           // words of a row
     auto turn = [](int row) { return (row / kWord) & 3; };
