@@ -294,3 +294,16 @@ def test_two_streams_at_once(w8, kind, kernel, M, E, N, K):
     torch.cuda.synchronize()
     for i in range(3):
         assert torch.equal(outs[0][i], want[0]) and torch.equal(outs[1][i], want[1]), i
+
+
+@pytest.mark.parametrize("kind,kernel,M,E,N,K", SEVERAL)
+def test_rows_of_an_x_that_has_none(w8, kind, kernel, M, E, N, K):
+    """Every index is outside x, whose tensors have no storage: the bias alone."""
+    _named(w8, kind, kernel, M, E, N, K)
+    c = Whole(kind, 1, E, N, K, seed=kernel + 9)
+    c.xq, c.xs = c.xq[:0].clone(), c.xs[:0].clone()
+    offsets = _even(M, E)
+    rows = torch.arange(-1, M - 1, dtype=torch.int32, device="cuda")
+    y = c.run(w8, _device(offsets), rows, c.bias)
+    group = torch.cat([torch.full((b - a,), g, device="cuda") for g, a, b in ref.groups_of(offsets, M)])
+    assert torch.equal(y, c.bias[group])
